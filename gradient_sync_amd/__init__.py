@@ -16,6 +16,12 @@ Calls (same names and meaning as the C ABI):
   dp_fsdp_layer(x_local, w_shard, dy_local, w_full, y_local, dw_full, dw_shard, stream=None,
                 dx_local=None)                # dx_local: dp_fsdp_layer_ex
   dp_gemm_bf16(a, b, c, stream=None)          # c = a @ b (b_layout="nk": a @ b.T)
+
+The optimizer step and the 4-bit block-scaled product (training.py):
+  GradNorm(grads).run(max_norm)               # dp_grad_norm: norm, clip factor, step count
+  AdamW(params, grads, m, v, ...).step(...)   # dp_adamw / dp_adamw8 over many tensors
+  dp_mxfp4_quantize(x, transposed="no"), dp_mxfp4_dequantize(q)
+  dp_gemm_mxfp4(a, b), dp_mxfp4_linear(x, w)  # a . b^T; x quantised on the way
 """
 from __future__ import annotations
 
@@ -31,7 +37,9 @@ __all__ = [
     "dp_reduce_scatter_ex", "dp_all_gather_ex", "dp_all_reduce_ex", "dp_gemm_bf16_ex",
     "dp_weighted_reduce_ex", "dp_scatter_accumulate", "dp_settle", "GradPiece", "HipEvents",
     "dp_backward_allreduce_overlap", "dp_reduce_scatter_all_gather", "dp_fsdp_layer_static",
-    "DP_STATIC_SCRATCH_BYTES",
+    "DP_STATIC_SCRATCH_BYTES", "StepCtrl", "GradNorm", "AdamW", "AdamWOpts", "Mxfp4",
+    "dp_grad_norm", "dp_adamw", "dp_mxfp4_quantize", "dp_mxfp4_dequantize", "dp_gemm_mxfp4",
+    "dp_mxfp4_linear",
 ]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -49,7 +57,10 @@ EXPORTS = ("dp_shard_len", "dp_status_string", "dp_last_hip_error", "dp_version"
            "dp_fsdp_layer", "dp_gemm_bf16", "dp_reduce_scatter_ex", "dp_all_gather_ex",
            "dp_all_reduce_ex", "dp_gemm_bf16_ex", "dp_weighted_reduce_ex",
            "dp_scatter_accumulate", "dp_settle", "dp_backward_allreduce_overlap",
-           "dp_reduce_scatter_all_gather", "dp_fsdp_layer_ex", "dp_fsdp_layer_static")
+           "dp_reduce_scatter_all_gather", "dp_fsdp_layer_ex", "dp_fsdp_layer_static",
+           "dp_grad_norm", "dp_adamw", "dp_adamw8", "dp_mxfp4_code_bytes",
+           "dp_mxfp4_scale_bytes", "dp_mxfp4_quantize", "dp_mxfp4_dequantize", "dp_gemm_mxfp4",
+           "dp_mxfp4_linear_ws_bytes", "dp_mxfp4_linear")
 
 _DTYPES = {torch.float32: DP_F32, torch.bfloat16: DP_BF16, torch.int32: DP_I32}
 _OPS = {"sum": DP_SUM, "avg": DP_AVG}
@@ -186,6 +197,27 @@ def lib():
         L.dp_backward_allreduce_overlap.argtypes = [
             _int, _int, _vp, _i64, _vp, _vp, _vp, _vp, _i64, _i64, _int, P, _vp, _vp, _vp, _int]
         L.dp_settle.argtypes = [_vp, _vp, _sz, _int, _int, ctypes.c_float, _int, _vp]
+        L.dp_grad_norm.restype = _int
+        L.dp_grad_norm.argtypes = [_int, _vp, _vp, _int, ctypes.c_double, _vp, _vp, _vp]
+        L.dp_adamw.restype = _int
+        L.dp_adamw.argtypes = [_int, _vp, _vp, _int, _vp, _int] + [_vp] * 6
+        L.dp_adamw8.restype = _int
+        L.dp_adamw8.argtypes = [_int, _vp, _vp, _int, _vp, _int] + [_vp] * 7
+        L.dp_mxfp4_code_bytes.restype = _sz
+        L.dp_mxfp4_code_bytes.argtypes = [_i64, _i64]
+        L.dp_mxfp4_scale_bytes.restype = _sz
+        L.dp_mxfp4_scale_bytes.argtypes = [_i64, _i64]
+        L.dp_mxfp4_quantize.restype = _int
+        L.dp_mxfp4_quantize.argtypes = [_vp, _i64, _i64, _i64, _int] + [_vp] * 5
+        L.dp_mxfp4_dequantize.restype = _int
+        L.dp_mxfp4_dequantize.argtypes = [_vp, _vp, _i64, _i64, _vp, _i64, _int, _vp]
+        L.dp_gemm_mxfp4.restype = _int
+        L.dp_gemm_mxfp4.argtypes = [_vp] * 5 + [_i64, _i64, _i64, _int, _int, _vp]
+        L.dp_mxfp4_linear_ws_bytes.restype = _sz
+        L.dp_mxfp4_linear_ws_bytes.argtypes = [_i64, _i64]
+        L.dp_mxfp4_linear.restype = _int
+        L.dp_mxfp4_linear.argtypes = [_vp, _i64, _int, _vp, _vp, _vp, _i64, _i64, _i64, _int, _vp,
+                                      _vp]
         _lib = L
     return _lib
 
@@ -587,3 +619,8 @@ def dp_reduce_scatter_all_gather(rs_send, rs_recv, ag_send, ag_recv, op: str = "
                                               P(ag_recv), ag_n, k, _dt(rs_send[0]), _OPS[op],
                                               s_chunks, _stream(stream)),
            "dp_reduce_scatter_all_gather")
+
+
+from .training import (AdamW, AdamWOpts, GradNorm, Mxfp4, StepCtrl, dp_adamw,  # noqa: E402
+                       dp_gemm_mxfp4, dp_grad_norm, dp_mxfp4_dequantize, dp_mxfp4_linear,
+                       dp_mxfp4_quantize)

@@ -15,7 +15,8 @@ ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libdpsync.so")
 SOURCES = ["api.hip", "sync_kernels.hip", "gemm_f32.hip", "gemm_bf16.hip", "odc_kernels.hip",
-           "fsdp_kernels.hip"]
+           "fsdp_kernels.hip", "api_train.hip", "optim_kernels.hip", "mxfp4_quant.hip",
+           "mxfp4_gemm.hip"]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 ARCH = "gfx950"

@@ -514,6 +514,8 @@ dp_status_t scratch_base(char **base)
 
 }  // namespace
 
+int dps::hip_failure_code(hipError_t e) { return hip_status(e); }
+
 extern "C" {
 
 size_t dp_shard_len(size_t n, int k)

@@ -5,6 +5,10 @@
 
 namespace dps {
 
+// The status of a HIP call for the entry points, kept for dp_last_hip_error()
+// where it failed.
+int hip_failure_code(hipError_t e);
+
 // Batched fp32 GEMM on MFMA: for each batch b < nb,
 // C_b[M,N] = op(A_b)[M,Kd] * op(B_b)[Kd,N], row-major; op(A) = A ([M,Kd]) or,
 // with trans_a, A^T where A_b is stored [Kd,M]; op(B) = B ([Kd,N]) or, with

@@ -425,6 +425,168 @@ dp_status_t dp_scatter_accumulate(const void *const *grads, int np, int dt, floa
 dp_status_t dp_settle(float *const *acc, void *const *out, size_t n, int k, int dt, float divisor,
                       int reset, void *stream);
 
+/*
+ * The optimizer step of a sharded data-parallel update. Between the
+ * ReduceScatter that leaves each rank its gradient shards and the AllGather that
+ * collects the updated parameters, a rank bounds the gradient's norm and updates
+ * its shards. The calls below take a list of nt tensors (HOST arrays of nt
+ * DEVICE pointers and of nt element counts), of any sizes and element
+ * alignment, and run them in ceil(nt / 64) launches (the norm: nt / 128).
+ * Empty tensors are allowed and their pointers not looked at; nt = 0 is a
+ * no-op (the norm of nothing is 0).
+ */
+#define DP_MAX_TENSORS 65536
+#define DP_STATE_BLOCK 128            /* elements that share an 8-bit state's scales */
+#define DP_GRAD_NORM_WS_BYTES 16640
+
+/* Step control in DEVICE memory (4-byte aligned), written by dp_grad_norm and
+ * read by dp_adamw / dp_adamw8, so that neither clipping, nor skipping a bad
+ * step, nor counting steps needs the host, and a captured graph replays them. */
+typedef struct {
+    float norm;       /* the gradient's 2-norm */
+    float scale;      /* what the gradient is multiplied by; 0: the step is skipped */
+    int32_t step;     /* steps taken, this one included (the caller starts it at 0) */
+    int32_t skipped;  /* steps skipped because the norm was not finite */
+} dp_step_ctrl_t;
+
+/*
+ * norm = sqrt(sum of the squares of all elements of all tensors), summed in
+ * fp64 in a fixed order (the same bits in every run), and the clip factor:
+ *   finite norm : scale = max_norm / norm if max_norm > 0 and norm > max_norm,
+ *                 else 1; step += 1
+ *   otherwise   : scale = 0; skipped += 1
+ * (a norm beyond fp32 counts as not finite).
+ *   grads[i]  : counts[i] elements of dt (DP_F32 or DP_BF16)
+ *   workspace : DP_GRAD_NORM_WS_BYTES bytes of device memory, 8-byte aligned,
+ *               zeroed by the caller once before its first use. Calls that can
+ *               run at the same time need workspaces of their own.
+ * ctrl, workspace and the gradients must not overlap (DP_ERR_ALIAS).
+ */
+dp_status_t dp_grad_norm(int nt, const int64_t *counts, const void *const *grads, int dt,
+                         double max_norm, dp_step_ctrl_t *ctrl, void *workspace, void *stream);
+
+/*
+ * AdamW (decoupled weight decay) in fp32, for every element:
+ *   g = scale g               scale = ctrl->scale, or 1 without ctrl
+ *   m = beta1 m + (1 - beta1) g
+ *   v = beta2 v + (1 - beta2) g^2
+ *   p = p (1 - lr weight_decay)
+ *       - lr / (1 - beta1^t) * m / (sqrt(v) / sqrt(1 - beta2^t) + eps)
+ * with t = opts->step, or ctrl->step where opts->step is 0. With ctrl->scale = 0
+ * nothing is changed.
+ *   params[i] : p_dt, updated in place; DP_BF16 is rounded to nearest even
+ *   grads[i]  : g_dt
+ *   copies    : NULL, or for DP_F32 parameters bf16 copies of the new values
+ *               (what is gathered next); else DP_ERR_UNSUPPORTED
+ * No written buffer may overlap another buffer (DP_ERR_ALIAS).
+ */
+#define DP_ADAMW_STOCHASTIC 1         /* dp_adamw8: round the states at random */
+typedef struct {
+    double lr, beta1, beta2, eps, weight_decay;  /* lr, eps, weight_decay >= 0; 0 <= beta < 1 */
+    int64_t step;                                /* >= 1, or 0: ctrl->step (ctrl required) */
+    uint64_t seed;                               /* of the random rounding */
+    int flags;
+    int reserved;                                /* must be zero */
+} dp_adamw_opts_t;
+
+dp_status_t dp_adamw(int nt, const int64_t *counts, void *const *params, int p_dt,
+                     const void *const *grads, int g_dt, float *const *m, float *const *v,
+                     void *const *copies, const dp_adamw_opts_t *opts, const dp_step_ctrl_t *ctrl,
+                     void *stream);
+
+/*
+ * The same step with the states in 8 bits. Each block of DP_STATE_BLOCK
+ * consecutive elements of a tensor (the last may be short) has two fp32 scales,
+ * scales[i][2b] for m and scales[i][2b + 1] for the root of v (8-byte aligned):
+ *   m       = m_code * scales[2b]
+ *   sqrt(v) = v_code * scales[2b + 1]
+ * with codes in OCP e4m3 (4 exponent, 3 mantissa bits, largest 448). The
+ * new scales are the block's largest |m| and sqrt(v) over 448 (zero, with zero
+ * codes, where that largest value is below 2^-100). A positive sqrt(v) is
+ * never held as zero but at least as the smallest code. The parameters are
+ * updated from the new m and v before these are rounded. All-zero
+ * codes and scales are the initial state.
+ *   Rounding: to nearest even; with DP_ADAMW_STOCHASTIC to one of the two
+ *   neighbours, with probability in proportion, from 16 bits r of a
+ *   counter-based generator: |y| -> floor(|y| / u + r / 65536) u, u the step
+ *   of y's octave. The bits are those of mix(mix(mix(seed + t G) + (i + 1) G)
+ *   + (j + 1) G) for elements 2j, 2j + 1 of tensor i at step t (G =
+ *   0x9E3779B97F4A7C15, mix = SplitMix64's output function): m of 2j, v of
+ *   2j, m of 2j + 1, v of 2j + 1 from the lowest up. The same seed and step give
+ *   the same bits in every run.
+ */
+dp_status_t dp_adamw8(int nt, const int64_t *counts, void *const *params, int p_dt,
+                      const void *const *grads, int g_dt, uint8_t *const *m, uint8_t *const *v,
+                      float *const *scales, void *const *copies, const dp_adamw_opts_t *opts,
+                      const dp_step_ctrl_t *ctrl, void *stream);
+
+/*
+ * 4-bit floating point with a scale per block: 32 consecutive values of a row
+ * share a power-of-two scale 2^e (OCP Microscaling Formats v1.0, MXFP4: e2m1
+ * elements, e8m0 scales). With it a gathered weight is 17/32 byte a value
+ * against 2 for bf16, and the product runs at the matrix cores' 4-bit rate.
+ *   e    = max(floor(log2 max|x|) - 2, -127) over the block
+ *   code = x 2^-e rounded to nearest even over 0, .5, 1, 1.5, 2, 3, 4, 6 and
+ *          their negatives; above 5: 6
+ * A block with a NaN or an infinity is NaN as a whole (scale byte 255).
+ *
+ * Layout of a quantised [rows, cols] matrix (blocks along the columns):
+ *   codes  : rows of 64 * ceil(cols / 128) bytes, 16-byte aligned; value j in
+ *            bits 4 (j % 2) .. + 3 of byte j / 2, zero past cols
+ *   scales : e + 127 in one byte per block, in 256-byte tiles of 16 rows x 16
+ *            blocks, 4-byte aligned; row r, block b at byte
+ *            ((r / 16) * ceil(cols / 512) + b / 16) * 256
+ *            + (16 (b % 4) + r % 16) * 4 + (b % 16) / 4
+ *            (bytes of rows or blocks that do not exist are unspecified)
+ * Row shards of a multiple of 16 rows are contiguous in both, so dp_all_gather
+ * collects a quantised weight (as DP_I32: both sizes are multiples of 4).
+ */
+size_t dp_mxfp4_code_bytes(int64_t rows, int64_t cols);
+size_t dp_mxfp4_scale_bytes(int64_t rows, int64_t cols);
+
+/*
+ * Quantises src ([rows, cols], row stride ld >= cols elements, DP_F32 or
+ * DP_BF16, any element alignment) as it is into codes / scales, and its
+ * transpose ([cols, rows], blocks along the rows of src: the operand of a
+ * product that sums over them) into codes_t / scales_t. Either pair may be
+ * NULL. The outputs must not overlap src or one another (DP_ERR_ALIAS).
+ */
+dp_status_t dp_mxfp4_quantize(const void *src, int64_t rows, int64_t cols, int64_t ld, int dt,
+                              void *codes, void *scales, void *codes_t, void *scales_t,
+                              void *stream);
+
+/* The values that a quantised matrix stands for, into dst ([rows, cols], row
+ * stride ld, DP_F32 or DP_BF16: exact in both, bf16 down to its smallest
+ * subnormal). */
+dp_status_t dp_mxfp4_dequantize(const void *codes, const void *scales, int64_t rows, int64_t cols,
+                                void *dst, int64_t ld, int dt, void *stream);
+
+/*
+ * c[m,n] = a[m,kk] . b[n,kk]^T of quantised operands, summed in fp32; c is
+ * row-major and contiguous, DP_F32 or DP_BF16 (rounded once, to nearest even).
+ * With accumulate (DP_F32 only) the product is added to c. m or n = 0 is a
+ * no-op; kk >= 1; m n <= 2^40. c must not overlap an operand (DP_ERR_ALIAS).
+ * Training a linear layer y = x w^T on quantised operands:
+ *   y[m,n]  = Q(x) . Q(w)^T                quantised along k
+ *   dx[m,k] = Q(dy) . Q(w^T)^T             along n
+ *   dw[n,k] = Q(dy^T) . Q(x^T)^T           along m (the tokens)
+ */
+dp_status_t dp_gemm_mxfp4(const void *a, const void *a_scales, const void *b, const void *b_scales,
+                          void *c, int64_t m, int64_t n, int64_t kk, int c_dt, int accumulate,
+                          void *stream);
+
+/*
+ * y[m,n] = Q(x)[m,kk] . w[n,kk]^T with x plain (DP_F32 or DP_BF16, row stride
+ * ldx) and w quantised: dp_mxfp4_quantize and dp_gemm_mxfp4 in one call, the
+ * same bits. Up to 16 rows (single tokens) x is quantised inside the product, in
+ * one launch and without a workspace; beyond, the workspace holds Q(x):
+ * dp_mxfp4_linear_ws_bytes(m, kk) bytes, 16-byte aligned.
+ */
+size_t dp_mxfp4_linear_ws_bytes(int64_t m, int64_t kk);
+dp_status_t dp_mxfp4_linear(const void *x, int64_t ldx, int x_dt, const void *w,
+                            const void *w_scales, void *y, int64_t m, int64_t n, int64_t kk,
+                            int y_dt, void *workspace, void *stream);
+
 #ifdef __cplusplus
 }
 #endif
