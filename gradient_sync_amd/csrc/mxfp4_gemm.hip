@@ -9,6 +9,8 @@
 // that block's scale. D register r of lane l: D[4 (l / 16) + r][l % 16]. The
 // instruction gets B's rows first, so that a lane ends with 4 consecutive
 // columns of one row of C.
+#include <type_traits>
+
 #include "mxfp4_device.h"
 
 namespace dps {
@@ -202,10 +204,289 @@ hipError_t launch_few(const MxGemmParams &p, int x_dt, hipStream_t stream)
     return hipGetLastError();
 }
 
+// ------------------------------------------------------------ tiled kernel
+
+#define MX_FENCE() __builtin_amdgcn_sched_barrier(0)
+
+// Workgroup id -> tile of C: ids go round-robin to the 8 XCDs, so each XCD is
+// handed a contiguous range of tiles, 4 tile rows at a time, and its L2 holds
+// the rows of A and B that its workgroups share.
+__device__ __forceinline__ void tile_of(int id, int tiles_m, int tiles_n, int &tm, int &tn)
+{
+    const int total = tiles_m * tiles_n;
+    constexpr int XCDS = 8, GROUP = 4;
+    if (total % XCDS == 0) id = (id % XCDS) * (total / XCDS) + id / XCDS;
+    const int g = id / (GROUP * tiles_n), first = g * GROUP;
+    const int rows = min(GROUP, tiles_m - first), in = id - g * GROUP * tiles_n;
+    tm = first + in % rows;
+    tn = in / rows;
+}
+
+typedef __attribute__((address_space(3))) void lds_void;
+
+// The matrix instruction with its sums in the accumulation registers for good:
+// left to the compiler, part of the 256 sums of the large tile sit in other
+// registers and are copied around every pass of the loop. The compiler sees
+// neither the instruction's latency nor its hazards, so a read of the sums and a
+// write of an operand by a vector instruction are kept apart from it by
+// mx_settle() below. Scale byte T of both operands.
+template <int T>
+__device__ __forceinline__ void mfma_acc(f32x4 &c, u32x4 first, unsigned fs, u32x4 second, unsigned ss)
+{
+#define MX_MFMA(sel)                                                                       \
+    asm volatile("v_mfma_scale_f32_16x16x128_f8f6f4 %0, %1, %2, %0, %3, %4 " sel " cbsz:4 blgp:4" \
+                 : "+a"(c) : "v"(first), "v"(second), "v"(fs), "v"(ss))
+    if constexpr (T == 0)
+        MX_MFMA("op_sel_hi:[0,0,0]");
+    else if constexpr (T == 1)
+        MX_MFMA("op_sel:[1,1,0] op_sel_hi:[0,0,0]");
+    else if constexpr (T == 2)
+        MX_MFMA("op_sel_hi:[1,1,0]");
+    else
+        MX_MFMA("op_sel:[1,1,0] op_sel_hi:[1,1,0]");
+#undef MX_MFMA
+}
+// names a value as one in a vector register at this point
+__device__ __forceinline__ void mx_pin(unsigned &x)
+{
+    asm volatile("" : "+v"(x));
+}
+// 32 cycles: longer than the instruction takes to write its sums (16) and than
+// a vector instruction's result takes to reach it
+__device__ __forceinline__ void mx_settle() { asm volatile("s_nop 15\n\ts_nop 15" ::: "memory"); }
+
+// Tile of 32 WB x 32 WB, 4 waves of 16 WB x 16 WB (WB x WB instructions per
+// 128-wide step of K). A stage is 256 of K, 128 bytes a row, and goes from
+// global memory straight into one of two LDS buffers (buffer_load ... lds, 8
+// rows an instruction): chunk c (16 bytes, one block) of row r sits at position
+// c ^ (r % 8), so the 16 rows that a fragment read touches at one chunk hit
+// distinct banks. Stage t is computed in two steps: step 0 while the fragments
+// of step 1 are read; then each wave waits for its loads of stage t + 1 and the
+// workgroup meets; then step 1 while the first fragments of stage t + 1 are
+// read and the loads of stage t + 2 go into the buffer just left.
+//
+// Scales come as one 32-bit load per 16 rows and two stages (their layout is
+// the operand's), loaded a pair of stages ahead and kept in registers.
+//
+// K is walked in pairs of stages (512). In the last pair the steps past K get
+// scale bytes of zero on both sides: whatever codes stand there (those of the
+// next row, or of the operand's end; every code is a finite number), their
+// products are at most 2^-254 * 36 each and vanish against fp32's smallest
+// 2^-149. Rows past M or N are loads of the last row, and their results are not
+// stored.
+template <int WB, int CT, bool VEC>
+__global__ __launch_bounds__(256) void mxfp4_gemm_tile_kernel(const MxGemmParams p, int tiles_m, int tiles_n)
+{
+#ifdef __HIP_DEVICE_COMPILE__                        // the host pass rejects the body's operands, and needs none
+    constexpr int T = 32 * WB;                       // tile side
+    constexpr int BYTES = T * 128;
+    __shared__ __attribute__((aligned(1024))) unsigned char A0[BYTES], A1[BYTES], B0[BYTES], B1[BYTES];
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int wi = wave >> 1, wj = wave & 1, i = lane & 15, g = lane >> 4;
+    int tm, tn;
+    tile_of(blockIdx.x, tiles_m, tiles_n, tm, tn);
+    const long long m0 = (long long)tm * T, n0 = (long long)tn * T;
+    const int rows_a = (int)min((long long)T, p.m - m0), rows_b = (int)min((long long)T, p.n - n0);
+    const int pitch = (int)mx_pitch(p.k), ktiles = (int)mx_scale_tiles(p.k);
+    const int steps = (int)((p.k + 127) / 128), pairs = (steps + 3) / 4;
+    const unsigned tail = ~0u >> (8 * (pairs * 4 - steps));
+    auto abuf = [&](int buf) __attribute__((always_inline)) { return buf ? A1 : A0; };
+    auto bbuf = [&](int buf) __attribute__((always_inline)) { return buf ? B1 : B0; };
+
+    // byte offsets within a tile's rows fit 31 bits (checked by the launcher)
+    const __amdgpu_buffer_rsrc_t rA =
+        __builtin_amdgcn_make_buffer_rsrc((void *)(p.a + m0 * pitch), (short)0, 0x7fffffff, 0x00020000);
+    const __amdgpu_buffer_rsrc_t rB =
+        __builtin_amdgcn_make_buffer_rsrc((void *)(p.b + n0 * pitch), (short)0, 0x7fffffff, 0x00020000);
+    const int lr = lane >> 3;
+    int off[2 * WB];
+#pragma unroll
+    for (int q = 0; q < 2 * WB; ++q) {
+        const int row = wave * 8 * WB + (q % WB) * 8 + lr;
+        off[q] = min(row, (q < WB ? rows_a : rows_b) - 1) * pitch + (((lane & 7) ^ lr) << 4);
+    }
+    auto dtl = [&](int buf, int stage, int q) __attribute__((always_inline)) {
+        const int row0 = wave * 8 * WB + (q % WB) * 8;
+        if (q < WB)
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(rA, (lds_void *)(abuf(buf) + row0 * 128), 16,
+                                                     min(off[q] + stage * 128, rows_a * pitch - 16), 0, 0, 0);
+        else
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(rB, (lds_void *)(bbuf(buf) + row0 * 128), 16,
+                                                     min(off[q] + stage * 128, rows_b * pitch - 16), 0, 0, 0);
+    };
+    // scales of 16-row group x of this wave's rows of A or B, pair of stages kt
+    const long long ga = m0 / 16 + wi * WB, gb = n0 / 16 + wj * WB;
+    const long long last_ga = (p.m - 1) / 16, last_gb = (p.n - 1) / 16;
+    auto scale_a = [&](int x, int kt) __attribute__((always_inline)) {
+        const unsigned char *at = p.a_scales + (min(ga + x, last_ga) * ktiles + kt) * 256;
+        return reinterpret_cast<const unsigned *>(at)[lane];
+    };
+    auto scale_b = [&](int x, int kt) __attribute__((always_inline)) {
+        const unsigned char *at = p.b_scales + (min(gb + x, last_gb) * ktiles + kt) * 256;
+        return reinterpret_cast<const unsigned *>(at)[lane];
+    };
+
+    f32x4 acc[WB][WB];
+#pragma unroll
+    for (int a = 0; a < WB; ++a)
+#pragma unroll
+        for (int b = 0; b < WB; ++b) {
+            acc[a][b] = f32x4{};
+            asm volatile("" : "+a"(acc[a][b]));
+        }
+    mx_settle();
+    u32x4 af[2][WB], bf[2][WB];
+    unsigned sa[WB], sb[WB], na[WB], nb[WB];
+
+    const int last = 2 * pairs - 1;
+#pragma unroll
+    for (int q = 0; q < 2 * WB; ++q) dtl(0, 0, q);
+#pragma unroll
+    for (int q = 0; q < 2 * WB; ++q) dtl(1, 1, q);
+#pragma unroll
+    for (int x = 0; x < WB; ++x) {
+        sa[x] = scale_a(x, 0) & (pairs == 1 ? tail : ~0u);
+        sb[x] = scale_b(x, 0) & (pairs == 1 ? tail : ~0u);
+        mx_pin(sa[x]);
+        mx_pin(sb[x]);
+    }
+    mx_settle();
+
+    // fragment read q of a step: q < WB B's block q, else A's block q - WB
+    const int fp = i * 128, fx = lane & 7;
+    auto rdq = [&](int set, int buf, int ks, int q) __attribute__((always_inline)) {
+        const int x = q % WB;
+        const int at = fp + (((ks * 4 + g) ^ fx) << 4);
+        if (q >= WB)
+            af[set][x] = *reinterpret_cast<const u32x4 *>(abuf(buf) + (wi * WB + x) * 2048 + at);
+        else
+            bf[set][x] = *reinterpret_cast<const u32x4 *>(bbuf(buf) + (wj * WB + x) * 2048 + at);
+    };
+    constexpr int N = WB * WB, EV = WB / 2, DV = WB == 8 ? 3 : 2;   // instructions per step, per read, per load
+    // stage 2 kt + buf; `next`: the stage to load two ahead
+    auto stage = [&](auto buf_, int next, int next_kt) __attribute__((always_inline)) {
+        constexpr int buf = decltype(buf_)::value;
+#pragma unroll
+        for (int q = 0; q < N; ++q) {
+            if (q % EV == 0) rdq(1, buf, 1, q / EV);
+            mfma_acc<2 * buf>(acc[q / WB][q % WB], bf[0][q % WB], sb[q % WB], af[0][q / WB], sa[q / WB]);
+            MX_FENCE();
+        }
+        __builtin_amdgcn_s_waitcnt(0x0F70);   // vmcnt(0): this wave's loads of the next stage landed
+        __syncthreads();
+        MX_FENCE();
+#pragma unroll
+        for (int q = 0; q < N; ++q) {
+            if (q % EV == 0) rdq(0, buf ^ 1, 0, q / EV);
+            if (q % DV == 0 && q / DV < 2 * WB) dtl(buf, next, q / DV);
+            if constexpr (buf == 0) {
+                if (q % EV == 1) {
+                    const int x = q / EV;
+                    if (x < WB)
+                        na[x] = scale_a(x, next_kt);
+                    else
+                        nb[x - WB] = scale_b(x - WB, next_kt);
+                }
+            }
+            mfma_acc<2 * buf + 1>(acc[q / WB][q % WB], bf[1][q % WB], sb[q % WB], af[1][q / WB], sa[q / WB]);
+            MX_FENCE();
+        }
+    };
+    __builtin_amdgcn_s_waitcnt(0x0F70);
+    __syncthreads();
+#pragma unroll
+    for (int q = 0; q < 2 * WB; ++q) rdq(0, 0, 0, q);
+    MX_FENCE();
+    for (int kt = 0; kt < pairs; ++kt) {
+        // past the end the loads repeat the last stage into a buffer that is not read again
+        stage(std::integral_constant<int, 0>{}, min(2 * kt + 2, last), min(kt + 1, pairs - 1));
+        stage(std::integral_constant<int, 1>{}, min(2 * kt + 3, last), 0);
+        mx_settle();
+        const unsigned keep = kt + 2 == pairs ? tail : ~0u;
+#pragma unroll
+        for (int x = 0; x < WB; ++x) {
+            sa[x] = na[x] & keep;
+            sb[x] = nb[x] & keep;
+            mx_pin(sa[x]);
+            mx_pin(sb[x]);
+        }
+        mx_settle();
+    }
+    __builtin_amdgcn_s_waitcnt(0x0F70);   // no load may land in LDS that is another workgroup's
+    mx_settle();
+#pragma unroll
+    for (int a = 0; a < WB; ++a)
+#pragma unroll
+        for (int b = 0; b < WB; ++b) asm volatile("" : "+a"(acc[a][b]));
+
+    // C: lane (i, g) holds columns 4 g .. 4 g + 3 of row i of each block
+    const long long row = m0 + wi * 16 * WB + i, col = n0 + wj * 16 * WB;
+    if constexpr (VEC && CT == kBF16) {
+        // pairs of blocks trade halves between lane rows g and g ^ 1, so that a
+        // lane holds 8 consecutive columns: one 16-byte store
+        typedef unsigned short u16;
+        const long long c8 = col + 16 * (g & 1) + 8 * (g >> 1);
+        u16 *c = reinterpret_cast<u16 *>(p.c) + row * p.n + c8;
+#pragma unroll
+        for (int a = 0; a < WB; ++a)
+#pragma unroll
+            for (int b = 0; b < WB; b += 2) {
+                const f32x4 x = acc[a][b], y = acc[a][b + 1];
+                const mx_f32x2 x0 = {x[0], x[1]}, x1 = {x[2], x[3]}, y0 = {y[0], y[1]}, y1 = {y[2], y[3]};
+                const auto s0 = __builtin_amdgcn_permlane16_swap(
+                    __builtin_bit_cast(unsigned, __builtin_convertvector(x0, mx_bf16x2)),
+                    __builtin_bit_cast(unsigned, __builtin_convertvector(y0, mx_bf16x2)), false, false);
+                const auto s1 = __builtin_amdgcn_permlane16_swap(
+                    __builtin_bit_cast(unsigned, __builtin_convertvector(x1, mx_bf16x2)),
+                    __builtin_bit_cast(unsigned, __builtin_convertvector(y1, mx_bf16x2)), false, false);
+                const u32x4 v = {s0[0], s1[0], s0[1], s1[1]};
+                if (row + a * 16 < p.m && c8 + b * 16 < p.n)
+                    *reinterpret_cast<u32x4 *>(c + (long long)a * 16 * p.n + b * 16) = v;
+            }
+    } else if constexpr (VEC) {
+        float *c = reinterpret_cast<float *>(p.c) + row * p.n + col + 4 * g;
+#pragma unroll
+        for (int a = 0; a < WB; ++a)
+#pragma unroll
+            for (int b = 0; b < WB; ++b)
+                if (row + a * 16 < p.m && col + 4 * g + b * 16 < p.n) {
+                    f32x4 *at = reinterpret_cast<f32x4 *>(c + (long long)a * 16 * p.n + b * 16);
+                    *at = p.accumulate ? *at + acc[a][b] : acc[a][b];
+                    MX_FENCE();
+                }
+    } else {
+#pragma unroll
+        for (int a = 0; a < WB; ++a)
+#pragma unroll
+            for (int b = 0; b < WB; ++b) store_c<CT>(p, row + a * 16, col + b * 16 + 4 * g, acc[a][b]);
+    }
+#endif
+}
+
+template <int WB, int CT>
+hipError_t launch_tile(const MxGemmParams &p, hipStream_t stream)
+{
+    const int T = 32 * WB;
+    const int tm = (int)((p.m + T - 1) / T), tn = (int)((p.n + T - 1) / T);
+    const bool vec = (uintptr_t)p.c % 16 == 0 && p.n % (CT == kBF16 ? 8 : 4) == 0;
+    if (vec)
+        mxfp4_gemm_tile_kernel<WB, CT, true><<<tm * tn, 256, 0, stream>>>(p, tm, tn);
+    else
+        mxfp4_gemm_tile_kernel<WB, CT, false><<<tm * tn, 256, 0, stream>>>(p, tm, tn);
+    return hipGetLastError();
+}
+
 template <int CT>
 hipError_t launch_typed(const MxGemmParams &p, int x_dt, hipStream_t stream)
 {
-    return p.m <= 16 ? launch_few<1, CT>(p, x_dt, stream) : launch_few<4, CT>(p, x_dt, stream);
+    if (p.m <= 16) return launch_few<1, CT>(p, x_dt, stream);
+    // the tiled kernels' offsets within a tile are 31 bits
+    if (p.m > 64 && mx_pitch(p.k) * 260 <= 0x7fffffffLL) {
+        const long long big = ((p.m + 255) / 256) * ((p.n + 255) / 256);
+        return big >= 160 ? launch_tile<8, CT>(p, stream) : launch_tile<4, CT>(p, stream);
+    }
+    return launch_few<4, CT>(p, x_dt, stream);
 }
 
 }  // namespace

@@ -214,6 +214,23 @@ def test_product_is_exact_for_small_integers(m, n, k):
     assert torch.equal(out, before + c)
 
 
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("m,n,k", [(4096, 2560, 512), (4001, 2500, 1100), (3900, 2601, 640), (2561, 4090, 130)])
+def test_product_of_large_matrices(m, n, k, dtype):
+    """Enough of C for the large tile, with and without edges, rows of C on 16 bytes or not."""
+    a, b = dps.dp_mxfp4_quantize(rand((m, k), 1)), dps.dp_mxfp4_quantize(rand((n, k), 2))
+    buf = torch.full((m * n + 64,), 5.0, dtype=dtype, device=DEV)
+    out = buf[32:32 + m * n].view(m, n)
+    say("large product", m, n, k, dtype)
+    dps.dp_gemm_mxfp4(a, b, out=out)
+    first = out.clone()
+    check_product(out, values(a), values(b), dtype=dtype)
+    if dtype == F32:
+        dps.dp_gemm_mxfp4(a, b, out=out, accumulate=True)
+        assert torch.equal(out, first + first)
+    assert bool((buf[:32] == 5).all()) and bool((buf[-32:] == 5).all())
+
+
 def test_product_of_extreme_scales_and_nan_blocks():
     a, b = rand((70, 160), 3), rand((50, 160), 4)
     a[:, 32:64] *= 2.0 ** 60
