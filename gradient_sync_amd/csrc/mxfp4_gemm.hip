@@ -246,6 +246,17 @@ __device__ __forceinline__ void mfma_acc(f32x4 &c, u32x4 first, unsigned fs, u32
         MX_MFMA("op_sel:[1,1,0] op_sel_hi:[1,1,0]");
 #undef MX_MFMA
 }
+// at most `newer` loads of this wave on their way, none of its LDS reads
+__device__ __forceinline__ void mx_wait(int newer)
+{
+    switch (newer) {
+#define MX_CASE(n) \
+    case n: __builtin_amdgcn_s_waitcnt(((n) & 15) | 0x70 | ((n) >> 4 << 14)); break;
+        MX_CASE(0) MX_CASE(4) MX_CASE(8) MX_CASE(9) MX_CASE(11) MX_CASE(18) MX_CASE(19)
+#undef MX_CASE
+    default: __builtin_unreachable();
+    }
+}
 // names a value as one in a vector register at this point
 __device__ __forceinline__ void mx_pin(unsigned &x)
 {
@@ -261,19 +272,23 @@ __device__ __forceinline__ void mx_settle() { asm volatile("s_nop 15\n\ts_nop 15
 // rows an instruction): chunk c (16 bytes, one block) of row r sits at position
 // c ^ (r % 8), so the 16 rows that a fragment read touches at one chunk hit
 // distinct banks. Stage t is computed in two steps: step 0 while the fragments
-// of step 1 are read; then each wave waits for its loads of stage t + 1 and the
-// workgroup meets; then step 1 while the first fragments of stage t + 1 are
-// read and the loads of stage t + 2 go into the buffer just left.
+// of step 1 are read; then step 1 while the first fragments of stage t + 1 are
+// read, B's and then A's, and the loads of stage t + 2 go into the buffer just
+// left, B's and then A's. Each wave waits for its loads of B of stage t + 1 and
+// the workgroup meets before step 1, and the same for A half way through it:
+// the later a load is issued, the later it is needed.
 //
 // Scales come as one 32-bit load per 16 rows and two stages (their layout is
 // the operand's), loaded a pair of stages ahead and kept in registers.
 //
-// K is walked in pairs of stages (512). In the last pair the steps past K get
-// scale bytes of zero on both sides: whatever codes stand there (those of the
-// next row, or of the operand's end; every code is a finite number), their
-// products are at most 2^-254 * 36 each and vanish against fp32's smallest
-// 2^-149. Rows past M or N are loads of the last row, and their results are not
-// stored.
+// K is walked in pairs of stages (512). In the last pair a stage past the row's
+// end is loaded from the row's last 128 bytes instead, so that no load leaves
+// the operand; a half stage then stands in the second half of its buffer. Steps
+// without data get scale bytes of zero on both sides: whatever codes stand there
+// (each is a finite number), their products are at most 2^-254 * 36 and
+// vanish against fp32's smallest 2^-149. One byte permutation with a scalar
+// selector does both. Rows past M or N are loads of the last row, and their
+// results are not stored.
 template <int WB, int CT, bool VEC>
 __global__ __launch_bounds__(256) void mxfp4_gemm_tile_kernel(const MxGemmParams p, int tiles_m, int tiles_n)
 {
@@ -290,7 +305,9 @@ __global__ __launch_bounds__(256) void mxfp4_gemm_tile_kernel(const MxGemmParams
     const int rows_a = (int)min((long long)T, p.m - m0), rows_b = (int)min((long long)T, p.n - n0);
     const int pitch = (int)mx_pitch(p.k), ktiles = (int)mx_scale_tiles(p.k);
     const int steps = (int)((p.k + 127) / 128), pairs = (steps + 3) / 4;
-    const unsigned tail = ~0u >> (8 * (pairs * 4 - steps));
+    // selection of the last pair's scale bytes (see above; 0x0c selects a zero byte)
+    const int rest = steps % 4;
+    const unsigned tail = rest == 0 ? 0x03020100u : rest == 1 ? 0x0c0c000cu : rest == 2 ? 0x0c0c0100u : 0x020c0100u;
     auto abuf = [&](int buf) __attribute__((always_inline)) { return buf ? A1 : A0; };
     auto bbuf = [&](int buf) __attribute__((always_inline)) { return buf ? B1 : B0; };
 
@@ -304,27 +321,31 @@ __global__ __launch_bounds__(256) void mxfp4_gemm_tile_kernel(const MxGemmParams
 #pragma unroll
     for (int q = 0; q < 2 * WB; ++q) {
         const int row = wave * 8 * WB + (q % WB) * 8 + lr;
-        off[q] = min(row, (q < WB ? rows_a : rows_b) - 1) * pitch + (((lane & 7) ^ lr) << 4);
+        off[q] = min(row, (q < WB ? rows_b : rows_a) - 1) * pitch + (((lane & 7) ^ lr) << 4);
     }
+    // a stage that reaches past the row is taken from the row's last 128 bytes
     auto dtl = [&](int buf, int stage, int q) __attribute__((always_inline)) {
         const int row0 = wave * 8 * WB + (q % WB) * 8;
+        const int so = __builtin_amdgcn_readfirstlane(min(stage * 128, pitch - 128));
         if (q < WB)
-            __builtin_amdgcn_raw_ptr_buffer_load_lds(rA, (lds_void *)(abuf(buf) + row0 * 128), 16,
-                                                     min(off[q] + stage * 128, rows_a * pitch - 16), 0, 0, 0);
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(rB, (lds_void *)(bbuf(buf) + row0 * 128), 16, off[q], so, 0, 0);
         else
-            __builtin_amdgcn_raw_ptr_buffer_load_lds(rB, (lds_void *)(bbuf(buf) + row0 * 128), 16,
-                                                     min(off[q] + stage * 128, rows_b * pitch - 16), 0, 0, 0);
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(rA, (lds_void *)(abuf(buf) + row0 * 128), 16, off[q], so, 0, 0);
     };
     // scales of 16-row group x of this wave's rows of A or B, pair of stages kt
-    const long long ga = m0 / 16 + wi * WB, gb = n0 / 16 + wj * WB;
-    const long long last_ga = (p.m - 1) / 16, last_gb = (p.n - 1) / 16;
-    auto scale_a = [&](int x, int kt) __attribute__((always_inline)) {
-        const unsigned char *at = p.a_scales + (min(ga + x, last_ga) * ktiles + kt) * 256;
-        return reinterpret_cast<const unsigned *>(at)[lane];
-    };
-    auto scale_b = [&](int x, int kt) __attribute__((always_inline)) {
-        const unsigned char *at = p.b_scales + (min(gb + x, last_gb) * ktiles + kt) * 256;
-        return reinterpret_cast<const unsigned *>(at)[lane];
+    const long long ga = m0 / 16, gb = n0 / 16;
+    const __amdgpu_buffer_rsrc_t sA =
+        __builtin_amdgcn_make_buffer_rsrc((void *)(p.a_scales + ga * ktiles * 256), (short)0, 0x7fffffff, 0x00020000);
+    const __amdgpu_buffer_rsrc_t sB =
+        __builtin_amdgcn_make_buffer_rsrc((void *)(p.b_scales + gb * ktiles * 256), (short)0, 0x7fffffff, 0x00020000);
+    int soff[2 * WB];
+#pragma unroll
+    for (int x = 0; x < WB; ++x) {
+        soff[x] = min(wi * WB + x, (rows_a - 1) >> 4) * ktiles * 256 + lane * 4;
+        soff[WB + x] = min(wj * WB + x, (rows_b - 1) >> 4) * ktiles * 256 + lane * 4;
+    }
+    auto scale = [&](int x, int kt) __attribute__((always_inline)) {      // x < WB: A's group x, else B's x - WB
+        return (unsigned)__builtin_amdgcn_raw_buffer_load_b32(x < WB ? sA : sB, soff[x], kt * 256, 0);
     };
 
     f32x4 acc[WB][WB];
@@ -337,22 +358,27 @@ __global__ __launch_bounds__(256) void mxfp4_gemm_tile_kernel(const MxGemmParams
         }
     mx_settle();
     u32x4 af[2][WB], bf[2][WB];
-    unsigned sa[WB], sb[WB], na[WB], nb[WB];
+    unsigned sa[WB], sb[WB], ns[2 * WB];
 
     const int last = 2 * pairs - 1;
 #pragma unroll
     for (int q = 0; q < 2 * WB; ++q) dtl(0, 0, q);
 #pragma unroll
     for (int q = 0; q < 2 * WB; ++q) dtl(1, 1, q);
+    const unsigned sel0 = pairs == 1 ? tail : 0x03020100u;
 #pragma unroll
     for (int x = 0; x < WB; ++x) {
-        sa[x] = scale_a(x, 0) & (pairs == 1 ? tail : ~0u);
-        sb[x] = scale_b(x, 0) & (pairs == 1 ? tail : ~0u);
+        sa[x] = __builtin_amdgcn_perm(0u, scale(x, 0), sel0);
+        sb[x] = __builtin_amdgcn_perm(0u, scale(WB + x, 0), sel0);
         mx_pin(sa[x]);
         mx_pin(sb[x]);
     }
     mx_settle();
 
+    auto take = [&](unsigned &x, unsigned next, unsigned sel) __attribute__((always_inline)) {
+        x = __builtin_amdgcn_perm(0u, next, sel);
+        mx_pin(x);
+    };
     // fragment read q of a step: q < WB B's block q, else A's block q - WB
     const int fp = i * 128, fx = lane & 7;
     auto rdq = [&](int set, int buf, int ks, int q) __attribute__((always_inline)) {
@@ -363,33 +389,48 @@ __global__ __launch_bounds__(256) void mxfp4_gemm_tile_kernel(const MxGemmParams
         else
             bf[set][x] = *reinterpret_cast<const u32x4 *>(bbuf(buf) + (wj * WB + x) * 2048 + at);
     };
-    constexpr int N = WB * WB, EV = WB / 2, DV = WB == 8 ? 3 : 2;   // instructions per step, per read, per load
-    // stage 2 kt + buf; `next`: the stage to load two ahead
-    auto stage = [&](auto buf_, int next, int next_kt) __attribute__((always_inline)) {
+    constexpr int N = WB * WB, EV = WB / 2, RV = WB == 8 ? 3 : 2, DV = RV;   // instructions per step, per read in step 1 and 0, per load
+    // In step 1's instructions stand, in this order, a load of B every DV, then
+    // those of A, and in even stages a scale load every EV. So many loads are
+    // newer than the last one of B (of A) where it has to have landed:
+    constexpr int kLoads = (N / 2 + DV - 1) / DV, kScales = (N / 2 + EV - 2) / EV;
+    constexpr int kScalesAfterB = 2 * WB - (DV * (WB - 1) + EV - 1) / EV;
+    // waits until at most `newer` of this wave's loads are on their way and its LDS reads are done, then for the others
+    auto meet = [&](int newer) __attribute__((always_inline)) {
+        MX_FENCE();
+        mx_wait(newer);
+        __builtin_amdgcn_s_barrier();
+        MX_FENCE();
+    };
+    // stage 2 kt + buf; `next`: the stage to load two ahead, `sel`: the next pair's selection of scale bytes
+    auto stage = [&](auto buf_, int next, int next_kt, unsigned sel) __attribute__((always_inline)) {
         constexpr int buf = decltype(buf_)::value;
 #pragma unroll
         for (int q = 0; q < N; ++q) {
-            if (q % EV == 0) rdq(1, buf, 1, q / EV);
+            if (q % RV == 0 && q / RV < 2 * WB) rdq(1, buf, 1, q / RV);
             mfma_acc<2 * buf>(acc[q / WB][q % WB], bf[0][q % WB], sb[q % WB], af[0][q / WB], sa[q / WB]);
             MX_FENCE();
         }
-        __builtin_amdgcn_s_waitcnt(0x0F70);   // vmcnt(0): this wave's loads of the next stage landed
-        __syncthreads();
-        MX_FENCE();
+        meet(WB + (buf == 1 ? kScalesAfterB : 0));                        // B of stage t + 1 is there
 #pragma unroll
         for (int q = 0; q < N; ++q) {
+            if (q == N / 2) meet(kLoads + (buf == 0 ? kScales : 0));      // A of stage t + 1 is there
             if (q % EV == 0) rdq(0, buf ^ 1, 0, q / EV);
-            if (q % DV == 0 && q / DV < 2 * WB) dtl(buf, next, q / DV);
             if constexpr (buf == 0) {
-                if (q % EV == 1) {
-                    const int x = q / EV;
-                    if (x < WB)
-                        na[x] = scale_a(x, next_kt);
-                    else
-                        nb[x - WB] = scale_b(x - WB, next_kt);
+                if (q % EV == 1) ns[q / EV] = scale(q / EV, next_kt);
+            }
+            if (q % DV == 0 && q / DV < 2 * WB) dtl(buf, next, q / DV);
+            mfma_acc<2 * buf + 1>(acc[q / WB][q % WB], bf[1][q % WB], sb[q % WB], af[1][q / WB], sa[q / WB]);
+            // the next pair's scales take their place as soon as this one's
+            // have been used, at least WB - 1 instructions before their first use
+            if constexpr (buf == 1) {
+                if (q % WB == 0 && q > 0) take(sa[q / WB - 1], ns[q / WB - 1], sel);
+                if (q > N - WB) take(sb[q - N + WB - 1], ns[WB + q - N + WB - 1], sel);
+                if (q == N - 1) {
+                    take(sa[WB - 1], ns[WB - 1], sel);
+                    take(sb[WB - 1], ns[2 * WB - 1], sel);
                 }
             }
-            mfma_acc<2 * buf + 1>(acc[q / WB][q % WB], bf[1][q % WB], sb[q % WB], af[1][q / WB], sa[q / WB]);
             MX_FENCE();
         }
     };
@@ -400,18 +441,8 @@ __global__ __launch_bounds__(256) void mxfp4_gemm_tile_kernel(const MxGemmParams
     MX_FENCE();
     for (int kt = 0; kt < pairs; ++kt) {
         // past the end the loads repeat the last stage into a buffer that is not read again
-        stage(std::integral_constant<int, 0>{}, min(2 * kt + 2, last), min(kt + 1, pairs - 1));
-        stage(std::integral_constant<int, 1>{}, min(2 * kt + 3, last), 0);
-        mx_settle();
-        const unsigned keep = kt + 2 == pairs ? tail : ~0u;
-#pragma unroll
-        for (int x = 0; x < WB; ++x) {
-            sa[x] = na[x] & keep;
-            sb[x] = nb[x] & keep;
-            mx_pin(sa[x]);
-            mx_pin(sb[x]);
-        }
-        mx_settle();
+        stage(std::integral_constant<int, 0>{}, min(2 * kt + 2, last), min(kt + 1, pairs - 1), 0u);
+        stage(std::integral_constant<int, 1>{}, min(2 * kt + 3, last), 0, kt + 2 == pairs ? tail : 0x03020100u);
     }
     __builtin_amdgcn_s_waitcnt(0x0F70);   // no load may land in LDS that is another workgroup's
     mx_settle();
@@ -446,15 +477,20 @@ __global__ __launch_bounds__(256) void mxfp4_gemm_tile_kernel(const MxGemmParams
             }
     } else if constexpr (VEC) {
         float *c = reinterpret_cast<float *>(p.c) + row * p.n + col + 4 * g;
+        auto each = [&](auto add) __attribute__((always_inline)) {
 #pragma unroll
-        for (int a = 0; a < WB; ++a)
+            for (int a = 0; a < WB; ++a)
 #pragma unroll
-            for (int b = 0; b < WB; ++b)
-                if (row + a * 16 < p.m && col + 4 * g + b * 16 < p.n) {
-                    f32x4 *at = reinterpret_cast<f32x4 *>(c + (long long)a * 16 * p.n + b * 16);
-                    *at = p.accumulate ? *at + acc[a][b] : acc[a][b];
-                    MX_FENCE();
-                }
+                for (int b = 0; b < WB; ++b)
+                    if (row + a * 16 < p.m && col + 4 * g + b * 16 < p.n) {
+                        f32x4 *at = reinterpret_cast<f32x4 *>(c + (long long)a * 16 * p.n + b * 16);
+                        *at = decltype(add)::value ? *at + acc[a][b] : acc[a][b];
+                    }
+        };
+        if (p.accumulate)
+            each(std::true_type{});
+        else
+            each(std::false_type{});
     } else {
 #pragma unroll
         for (int a = 0; a < WB; ++a)
@@ -481,8 +517,8 @@ template <int CT>
 hipError_t launch_typed(const MxGemmParams &p, int x_dt, hipStream_t stream)
 {
     if (p.m <= 16) return launch_few<1, CT>(p, x_dt, stream);
-    // the tiled kernels' offsets within a tile are 31 bits
-    if (p.m > 64 && mx_pitch(p.k) * 260 <= 0x7fffffffLL) {
+    // the tiled kernels need rows of 128 bytes, and offsets within a tile of 31 bits
+    if (p.m > 64 && p.k > 128 && mx_pitch(p.k) * 260 <= 0x7fffffffLL) {
         const long long big = ((p.m + 255) / 256) * ((p.n + 255) / 256);
         return big >= 160 ? launch_tile<8, CT>(p, stream) : launch_tile<4, CT>(p, stream);
     }
