@@ -8,7 +8,7 @@ namespace dps {
 
 // Workspace of the norm: one partial sum per workgroup, then the ticket that
 // tells the last workgroup to finish.
-constexpr int kNormMaxGrid = 2048;
+constexpr int kNormMaxGrid = 512;
 constexpr size_t kNormWsBytes = kNormMaxGrid * sizeof(double) + 64;
 
 // Device-side step control, laid out as dp_step_ctrl_t.

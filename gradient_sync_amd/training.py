@@ -18,7 +18,7 @@ import torch
 from . import _DTYPES, _check, _stream, lib, ptr_array
 
 STATE_BLOCK = 128               # DP_STATE_BLOCK in include/dpsync.h
-GRAD_NORM_WS_BYTES = 16640      # DP_GRAD_NORM_WS_BYTES
+GRAD_NORM_WS_BYTES = 4160      # DP_GRAD_NORM_WS_BYTES
 DP_ADAMW_STOCHASTIC = 1
 _FLOATS = (torch.float32, torch.bfloat16)
 _CODES = (torch.uint8, torch.float8_e4m3fn)

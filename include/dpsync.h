@@ -437,7 +437,7 @@ dp_status_t dp_settle(float *const *acc, void *const *out, size_t n, int k, int 
  */
 #define DP_MAX_TENSORS 65536
 #define DP_STATE_BLOCK 128            /* elements that share an 8-bit state's scales */
-#define DP_GRAD_NORM_WS_BYTES 16640
+#define DP_GRAD_NORM_WS_BYTES 4160
 
 /* Step control in DEVICE memory (4-byte aligned), written by dp_grad_norm and
  * read by dp_adamw / dp_adamw8, so that neither clipping, nor skipping a bad
