@@ -249,7 +249,8 @@ dp_status_t dp_mxfp4_quantize(const void *src, int64_t rows, int64_t cols, int64
     const int es = dps::elem_size(dt);
     if (!aligned(src, (uintptr_t)es) || (codes && !mx_operand_ok(codes, scales)) ||
         (codes_t && !mx_operand_ok(codes_t, scales_t)) ||
-        ((rows + 127) / 128) * ((cols + 127) / 128) > 0x7fffffffLL)
+        ((rows + 127) / 128) * ((cols + 127) / 128) > 0x3fffffffLL ||
+        (rows + 15) / 16 * dps::mx_scale_tiles(cols) > 0x7fffffffLL)
         return DP_ERR_INVALID_ARG;
     Range r[5];
     size_t n = 0;

@@ -9,6 +9,8 @@
 // that block's scale. D register r of lane l: D[4 (l / 16) + r][l % 16]. The
 // instruction gets B's rows first, so that a lane ends with 4 consecutive
 // columns of one row of C.
+#include <algorithm>
+#include <cmath>
 #include <type_traits>
 
 #include "mxfp4_device.h"
@@ -67,60 +69,58 @@ __device__ __forceinline__ void store_c(const MxGemmParams &p, long long row, lo
 template <int XT>
 __device__ __forceinline__ u32x4 quantize_block(const MxGemmParams &p, long long row, long long kb, unsigned &byte)
 {
-    unsigned x[32];
+    constexpr int W = XT == kBF16 ? 4 : 8;           // dwords per 8 values
+    unsigned x[4][W], top = 0;
     const long long c0 = kb * 32;
     const char *at = p.x + (row * p.ldx + c0) * (XT == kBF16 ? 2 : 4);
     if (c0 + 32 <= p.k) {
-        if constexpr (XT == kBF16) {
 #pragma unroll
-            for (int h = 0; h < 4; ++h) {
-                const u32x4 v = *reinterpret_cast<const mx_u32x4_e *>(at + 16 * h);
+        for (int h = 0; h < W; ++h) {
+            const u32x4 v = *reinterpret_cast<const mx_u32x4_e *>(at + 16 * h);
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    x[8 * h + 2 * i] = v[i] << 16;
-                    x[8 * h + 2 * i + 1] = v[i] & 0xffff0000u;
-                }
-            }
-        } else {
-#pragma unroll
-            for (int h = 0; h < 8; ++h) {
-                const u32x4 v = *reinterpret_cast<const mx_u32x4_e *>(at + 16 * h);
-#pragma unroll
-                for (int i = 0; i < 4; ++i) x[4 * h + i] = v[i];
-            }
+            for (int i = 0; i < 4; ++i) x[h * 4 / W][h * 4 % W + i] = v[i];
         }
     } else {
 #pragma unroll
-        for (int i = 0; i < 32; ++i) {
-            x[i] = 0;
-            if (c0 + i < p.k)
-                x[i] = XT == kBF16 ? (unsigned)reinterpret_cast<const unsigned short *>(at)[i] << 16
-                                   : reinterpret_cast<const unsigned *>(at)[i];
-        }
-    }
-    unsigned top = 0;
+        for (int i = 0; i < 4 * W; ++i) x[i / W][i % W] = 0;
 #pragma unroll
-    for (int i = 0; i < 32; ++i) top = max(top, x[i] & 0x7fffffffu);
+        for (int i = 0; i < 32; ++i)
+            if (c0 + i < p.k) {
+                if constexpr (XT == kBF16)
+                    x[i / 8][i % 8 / 2] |= (unsigned)reinterpret_cast<const unsigned short *>(at)[i] << (16 * (i & 1));
+                else
+                    x[i / 8][i % 8] = reinterpret_cast<const unsigned *>(at)[i];
+            }
+    }
+#pragma unroll
+    for (int i = 0; i < 4 * W; ++i)
+        top = XT == kBF16 ? mx_max_bf16x2(top, x[i / W][i % W]) : mx_max_f32(top, x[i / W][i % W]);
+    if constexpr (XT == kBF16) top = max(top << 16, top & 0xffff0000u);
     byte = mx_scale_byte(top);
-    const float inv = mx_inverse(byte);
+    const float scale = mx_scale(byte);
     u32x4 code;
 #pragma unroll
-    for (int o = 0; o < 4; ++o) {
-        float y[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) y[i] = __uint_as_float(x[8 * o + i]) * inv;
-        code[o] = byte == 255u ? 0u : mx_pack8(y);
-    }
+    for (int o = 0; o < 4; ++o) code[o] = byte == 255u ? 0u : mx_pack8(x[o], scale);
     return code;
 }
 
 // A workgroup computes 16 MB rows of C by 16 columns; its 4 waves take
-// 512-wide pieces of K in turn, straight from global memory, and their sums
-// meet in LDS in a fixed order.
+// 512-wide pieces of K in turn, two at a time, straight from global memory, and
+// their sums meet in LDS in a fixed order. B is read once, and reading it is
+// what the kernel's time is made of.
+//
+// XT >= 0 (up to 16 rows): A comes as plain values. While its pieces of B are on
+// their way, a wave quantises the blocks of A that they meet, one a lane, into
+// LDS in the operand's layout: with a block's lane as owner of the
+// matrix operand instead, all 16 rows' lanes would do the work of row 0 for a
+// single token.
+constexpr int kPieces = 2;
 template <int MB, int CT, int XT>
 __global__ __launch_bounds__(256) void mxfp4_gemm_few_kernel(const MxGemmParams p)
 {
     __shared__ f32x4 part[3][MB][64];
+    __shared__ __attribute__((aligned(16))) unsigned char xc[XT < 0 ? 1 : 4 * kPieces * 16 * 256];
+    __shared__ __attribute__((aligned(16))) unsigned char xs[XT < 0 ? 1 : 4 * kPieces * 256];
     const int lane = threadIdx.x & 63;
     // a scalar, so that what depends on it is skipped by a jump: the matrix
     // instructions run whatever the lane mask says
@@ -129,47 +129,69 @@ __global__ __launch_bounds__(256) void mxfp4_gemm_few_kernel(const MxGemmParams 
     const unsigned blocks_n = (unsigned)((p.n + 15) >> 4), bm = blockIdx.x / blocks_n;
     const long long n0 = (long long)(blockIdx.x - bm * blocks_n) * 16, m0 = (long long)bm * 16 * MB;
     const long long pitch = mx_pitch(p.k), tiles = mx_scale_tiles(p.k);
-    const long long steps = (p.k + 127) / 128;
+    const int steps = (int)((p.k + 127) / 128);
     const long long rb = min(n0 + i, p.n - 1);
     f32x4 acc[MB];
 #pragma unroll
     for (int b = 0; b < MB; ++b) acc[b] = f32x4{};
-    for (long long kt = wave; kt < tiles; kt += 4) {
-        const int here = (int)min(4LL, steps - kt * 4);
-        const unsigned bs = *reinterpret_cast<const unsigned *>(p.b_scales + ((n0 >> 4) * tiles + kt) * 256 + lane * 4);
-        u32x4 bw[4], aw[MB][4];
-        unsigned as[MB];
+    for (int kt0 = wave * kPieces; kt0 < (int)tiles; kt0 += 4 * kPieces) {
+        u32x4 bw[kPieces][4];
+        unsigned bs[kPieces];
 #pragma unroll
-        for (int t = 0; t < 4; ++t)
-            if (t < here) bw[t] = *reinterpret_cast<const u32x4 *>(p.b + rb * pitch + kt * 256 + t * 64 + g * 16);
+        for (int h = 0; h < kPieces; ++h) {
+            const int kt = kt0 + h, here = min(4, steps - kt * 4);
+            if (here <= 0) continue;
+            bs[h] = *reinterpret_cast<const unsigned *>(p.b_scales + ((n0 >> 4) * tiles + kt) * 256 + lane * 4);
 #pragma unroll
-        for (int b = 0; b < MB; ++b) {
-            const long long ra = min(m0 + b * 16 + i, p.m - 1);
-            if constexpr (XT < 0) {
-                // a row group past the last is the last one's: its rows are not stored
-                as[b] = *reinterpret_cast<const unsigned *>(p.a_scales + ((ra >> 4) * tiles + kt) * 256 + (g * 16 + (int)(ra & 15)) * 4);
+            for (int t = 0; t < 4; ++t)
+                if (t < here) bw[h][t] = *reinterpret_cast<const u32x4 *>(p.b + rb * pitch + kt * 256 + t * 64 + g * 16);
+        }
+        unsigned char *codes = xc + wave * (kPieces * 4096), *bytes = xs + wave * (kPieces * 256);
+        if constexpr (XT >= 0) {
+            const int blocks = (int)p.m * 16 * kPieces;
+            for (int id = lane; id < blocks; id += 64) {
+                const int row = id / (16 * kPieces), h = id / 16 % kPieces, bk = id % 16;
+                const long long kb = (kt0 + h) * 16LL + bk;
+                unsigned byte = 0;
+                u32x4 code = {};
+                if (kb * 32 < p.k) code = quantize_block<XT>(p, row, kb, byte);
+                *reinterpret_cast<u32x4 *>(codes + h * 4096 + row * 256 + bk * 16) = code;
+                bytes[h * 256 + mx_scale_at(row, bk, 1)] = (unsigned char)byte;
+            }
+            // the wave's own LDS operations are in order; nothing else touches its part
+            __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        }
 #pragma unroll
-                for (int t = 0; t < 4; ++t)
-                    if (t < here) aw[b][t] = *reinterpret_cast<const u32x4 *>(p.a + ra * pitch + kt * 256 + t * 64 + g * 16);
-            } else {
-                as[b] = 0;
+        for (int h = 0; h < kPieces; ++h) {
+            const int kt = kt0 + h, here = min(4, steps - kt * 4);
+            if (here <= 0) continue;
+            u32x4 aw[MB][4];
+            unsigned as[MB];
+#pragma unroll
+            for (int b = 0; b < MB; ++b) {
+                // rows past the last are the last one: they are not stored
+                const long long ra = min(m0 + b * 16 + i, p.m - 1);
+                const int at = (g * 16 + (int)(ra & 15)) * 4;
+                if constexpr (XT < 0)
+                    as[b] = *reinterpret_cast<const unsigned *>(p.a_scales + ((ra >> 4) * tiles + kt) * 256 + at);
+                else
+                    as[b] = *reinterpret_cast<const unsigned *>(bytes + h * 256 + at);
 #pragma unroll
                 for (int t = 0; t < 4; ++t)
                     if (t < here) {
-                        unsigned byte = 0;
-                        aw[b][t] = u32x4{};
-                        const long long kb = kt * 16 + t * 4 + g;
-                        if (kb * 32 < p.k) aw[b][t] = quantize_block<XT>(p, ra, kb, byte);
-                        as[b] |= byte << (8 * t);
+                        if constexpr (XT < 0)
+                            aw[b][t] = *reinterpret_cast<const u32x4 *>(p.a + ra * pitch + kt * 256 + t * 64 + g * 16);
+                        else
+                            aw[b][t] = *reinterpret_cast<const u32x4 *>(codes + h * 4096 + ra * 256 + t * 64 + g * 16);
                     }
             }
-        }
 #pragma unroll
-        for (int b = 0; b < MB; ++b) {
-            acc[b] = mfma<0>(bw[0], bs, aw[b][0], as[b], acc[b]);
-            if (here > 1) acc[b] = mfma<1>(bw[1], bs, aw[b][1], as[b], acc[b]);
-            if (here > 2) acc[b] = mfma<2>(bw[2], bs, aw[b][2], as[b], acc[b]);
-            if (here > 3) acc[b] = mfma<3>(bw[3], bs, aw[b][3], as[b], acc[b]);
+            for (int b = 0; b < MB; ++b) {
+                acc[b] = mfma<0>(bw[h][0], bs[h], aw[b][0], as[b], acc[b]);
+                if (here > 1) acc[b] = mfma<1>(bw[h][1], bs[h], aw[b][1], as[b], acc[b]);
+                if (here > 2) acc[b] = mfma<2>(bw[h][2], bs[h], aw[b][2], as[b], acc[b]);
+                if (here > 3) acc[b] = mfma<3>(bw[h][3], bs[h], aw[b][3], as[b], acc[b]);
+            }
         }
     }
     if (wave > 0) {
@@ -246,16 +268,11 @@ __device__ __forceinline__ void mfma_acc(f32x4 &c, u32x4 first, unsigned fs, u32
         MX_MFMA("op_sel:[1,1,0] op_sel_hi:[1,1,0]");
 #undef MX_MFMA
 }
-// at most `newer` loads of this wave on their way, none of its LDS reads
-__device__ __forceinline__ void mx_wait(int newer)
+// until at most NEWER loads of this wave are on their way and none of its LDS reads
+template <int NEWER>
+__device__ __forceinline__ void mx_wait()
 {
-    switch (newer) {
-#define MX_CASE(n) \
-    case n: __builtin_amdgcn_s_waitcnt(((n) & 15) | 0x70 | ((n) >> 4 << 14)); break;
-        MX_CASE(0) MX_CASE(4) MX_CASE(8) MX_CASE(9) MX_CASE(11) MX_CASE(18) MX_CASE(19)
-#undef MX_CASE
-    default: __builtin_unreachable();
-    }
+    __builtin_amdgcn_s_waitcnt((NEWER & 15) | 0x70 | (NEWER >> 4 << 14));
 }
 // names a value as one in a vector register at this point
 __device__ __forceinline__ void mx_pin(unsigned &x)
@@ -389,16 +406,16 @@ __global__ __launch_bounds__(256) void mxfp4_gemm_tile_kernel(const MxGemmParams
         else
             bf[set][x] = *reinterpret_cast<const u32x4 *>(bbuf(buf) + (wj * WB + x) * 2048 + at);
     };
-    constexpr int N = WB * WB, EV = WB / 2, RV = WB == 8 ? 3 : 2, DV = RV;   // instructions per step, per read in step 1 and 0, per load
+    constexpr int N = WB * WB, EV = WB / 2, RV = WB == 8 ? 3 : 2, DV = EV == 4 ? 4 : 2;   // instructions per step, per read in step 1 and 0, per load
     // In step 1's instructions stand, in this order, a load of B every DV, then
     // those of A, and in even stages a scale load every EV. So many loads are
     // newer than the last one of B (of A) where it has to have landed:
     constexpr int kLoads = (N / 2 + DV - 1) / DV, kScales = (N / 2 + EV - 2) / EV;
     constexpr int kScalesAfterB = 2 * WB - (DV * (WB - 1) + EV - 1) / EV;
-    // waits until at most `newer` of this wave's loads are on their way and its LDS reads are done, then for the others
-    auto meet = [&](int newer) __attribute__((always_inline)) {
+    // waits until at most that many of this wave's loads are on their way and its LDS reads are done, then for the others
+    auto meet = [&](auto newer) __attribute__((always_inline)) {
         MX_FENCE();
-        mx_wait(newer);
+        mx_wait<decltype(newer)::value>();
         __builtin_amdgcn_s_barrier();
         MX_FENCE();
     };
@@ -411,10 +428,10 @@ __global__ __launch_bounds__(256) void mxfp4_gemm_tile_kernel(const MxGemmParams
             mfma_acc<2 * buf>(acc[q / WB][q % WB], bf[0][q % WB], sb[q % WB], af[0][q / WB], sa[q / WB]);
             MX_FENCE();
         }
-        meet(WB + (buf == 1 ? kScalesAfterB : 0));                        // B of stage t + 1 is there
+        meet(std::integral_constant<int, WB + (buf == 1 ? kScalesAfterB : 0)>{});                        // B of stage t + 1 is there
 #pragma unroll
         for (int q = 0; q < N; ++q) {
-            if (q == N / 2) meet(kLoads + (buf == 0 ? kScales : 0));      // A of stage t + 1 is there
+            if (q == N / 2) meet(std::integral_constant<int, kLoads + (buf == 0 ? kScales : 0)>{});      // A of stage t + 1 is there
             if (q % EV == 0) rdq(0, buf ^ 1, 0, q / EV);
             if constexpr (buf == 0) {
                 if (q % EV == 1) ns[q / EV] = scale(q / EV, next_kt);
@@ -517,12 +534,24 @@ template <int CT>
 hipError_t launch_typed(const MxGemmParams &p, int x_dt, hipStream_t stream)
 {
     if (p.m <= 16) return launch_few<1, CT>(p, x_dt, stream);
+    if (p.m <= 32) return launch_few<2, CT>(p, x_dt, stream);
     // the tiled kernels need rows of 128 bytes, and offsets within a tile of 31 bits
-    if (p.m > 64 && p.k > 128 && mx_pitch(p.k) * 260 <= 0x7fffffffLL) {
-        const long long big = ((p.m + 255) / 256) * ((p.n + 255) / 256);
-        return big >= 160 ? launch_tile<8, CT>(p, stream) : launch_tile<4, CT>(p, stream);
-    }
-    return launch_few<4, CT>(p, x_dt, stream);
+    if (p.k <= 128 || mx_pitch(p.k) * 260 > 0x7fffffffLL) return launch_few<4, CT>(p, x_dt, stream);
+    // Microseconds, fitted to 40 shapes (m 33 .. 8192, n 1000 .. 14336, k 2000 ..
+    // 14336; each within a fifth of the measured times):
+    // few rows: 80 rows of codes per workgroup, one at 35 GB/s, all at 8.3 TB/s;
+    // tiles of 128: a stage of 256 takes a lone workgroup 0.42, and a CU with
+    //   several 0.62 each;
+    // tiles of 256: one workgroup a CU, 1.8 a stage and 5.5 to begin and end.
+    const double k = (double)p.k, stages = k / 256;
+    const double few = (double)((p.m + 63) / 64) * (double)((p.n + 15) / 16);
+    const double t128 = (double)((p.m + 127) / 128) * (double)((p.n + 127) / 128);
+    const double t256 = (double)((p.m + 255) / 256) * (double)((p.n + 255) / 256);
+    const double us_few = 2.0 + std::max(k * 1.16e-3, few * 40.0 * k / 8.3e6);
+    const double us_128 = 3.5 + stages * std::max(0.42, 0.62 * t128 / 256);
+    const double us_256 = std::ceil(t256 / 256) * (5.5 + 1.8 * stages);
+    if (us_few <= us_128 && us_few <= us_256) return launch_few<4, CT>(p, x_dt, stream);
+    return us_128 <= us_256 ? launch_tile<4, CT>(p, stream) : launch_tile<8, CT>(p, stream);
 }
 
 }  // namespace

@@ -472,10 +472,12 @@ template <int PT, int GT, bool S8, bool SR>
 __global__ __launch_bounds__(kNT) void adamw_kernel(const AdamParams k)
 {
     const int b = blockIdx.x;
-    // the last tensor that starts at or before this chunk: one a lane, in one load
-    static_assert(kAdamTensors == 64, "one tensor per lane");
-    const int lane = threadIdx.x & 63;
-    const int t = __popcll(__ballot(lane < k.nt && b >= k.first[lane])) - 1;
+    // the last tensor that starts at or before this chunk, by halves (one tensor a
+    // lane, a vector load and a ballot: 4% slower at 200M elements)
+    int t = 0;
+#pragma unroll
+    for (int half = kAdamTensors / 2; half > 0; half >>= 1)
+        if (t + half < k.nt && b >= k.first[t + half]) t += half;
     const long long at = (long long)(b - k.first[t]) * kAdamChunk;
     if (at + kAdamChunk <= k.t[t].n)
         adam_chunk<PT, GT, S8, SR, true>(k, k.t[t], t, at);
