@@ -22,6 +22,8 @@ typedef int i32x8 __attribute__((ext_vector_type(8)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef unsigned int u32x4 __attribute__((ext_vector_type(4)));
 
+#define MX_FENCE() __builtin_amdgcn_sched_barrier(0)
+
 template <int T>
 __device__ __forceinline__ f32x4 mfma(u32x4 first, unsigned fs, u32x4 second, unsigned ss, f32x4 c)
 {
@@ -31,7 +33,7 @@ __device__ __forceinline__ f32x4 mfma(u32x4 first, unsigned fs, u32x4 second, un
     return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, c, 4, 4, T, (int)fs, T, (int)ss);
 }
 
-// n (1..4) consecutive outputs of a row
+// 4 consecutive outputs of a row, fewer at its end; added to what is there with p.accumulate (fp32)
 template <int CT>
 __device__ __forceinline__ void store_c(const MxGemmParams &p, long long row, long long col, f32x4 v)
 {
@@ -45,7 +47,7 @@ __device__ __forceinline__ void store_c(const MxGemmParams &p, long long row, lo
             *reinterpret_cast<f32x4_e *>(c) = v;
         } else {
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
+            for (int i = 0; i < 3; ++i)
                 if (i < n) c[i] = p.accumulate ? c[i] + v[i] : v[i];
         }
     } else {
@@ -58,7 +60,7 @@ __device__ __forceinline__ void store_c(const MxGemmParams &p, long long row, lo
             *reinterpret_cast<u32x2_e *>(c) = u32x2_e{w[0], w[1]};
         } else {
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
+            for (int i = 0; i < 3; ++i)
                 if (i < n) c[i] = (unsigned short)(w[i >> 1] >> (16 * (i & 1)));
         }
     }
@@ -81,16 +83,26 @@ __device__ __forceinline__ u32x4 quantize_block(const MxGemmParams &p, long long
             for (int i = 0; i < 4; ++i) x[h * 4 / W][h * 4 % W + i] = v[i];
         }
     } else {
+        // the row's last, short block, in small loops: rare, and it must not cost the others registers
+        const int n = (int)(p.k - c0);
+        auto value = [&](int i) __attribute__((always_inline)) {     // i < n
+            return XT == kBF16 ? (unsigned)reinterpret_cast<const unsigned short *>(at)[i] << 16
+                               : reinterpret_cast<const unsigned *>(at)[i];
+        };
+#pragma unroll 1
+        for (int i = 0; i < n; ++i) top = mx_max_f32(top, value(i));
+        byte = mx_scale_byte(top);
+        u32x4 code = {};
+#pragma unroll 1
+        for (int o = 0; o < 4 && byte != 255u; ++o) {
+            unsigned y[8];
 #pragma unroll
-        for (int i = 0; i < 4 * W; ++i) x[i / W][i % W] = 0;
+            for (int i = 0; i < 8; ++i) y[i] = 8 * o + i < n ? value(8 * o + i) : 0u;
+            const unsigned w = mx_pack8(y, mx_scale(byte));
 #pragma unroll
-        for (int i = 0; i < 32; ++i)
-            if (c0 + i < p.k) {
-                if constexpr (XT == kBF16)
-                    x[i / 8][i % 8 / 2] |= (unsigned)reinterpret_cast<const unsigned short *>(at)[i] << (16 * (i & 1));
-                else
-                    x[i / 8][i % 8] = reinterpret_cast<const unsigned *>(at)[i];
-            }
+            for (int i = 0; i < 4; ++i) code[i] = i == o ? w : code[i];
+        }
+        return code;
     }
 #pragma unroll
     for (int i = 0; i < 4 * W; ++i)
@@ -227,8 +239,6 @@ hipError_t launch_few(const MxGemmParams &p, int x_dt, hipStream_t stream)
 }
 
 // ------------------------------------------------------------ tiled kernel
-
-#define MX_FENCE() __builtin_amdgcn_sched_barrier(0)
 
 // Workgroup id -> tile of C: ids go round-robin to the 8 XCDs, so each XCD is
 // handed a contiguous range of tiles, 4 tile rows at a time, and its L2 holds
@@ -470,7 +480,7 @@ __global__ __launch_bounds__(256) void mxfp4_gemm_tile_kernel(const MxGemmParams
 
     // C: lane (i, g) holds columns 4 g .. 4 g + 3 of row i of each block
     const long long row = m0 + wi * 16 * WB + i, col = n0 + wj * 16 * WB;
-    if constexpr (VEC && CT == kBF16) {
+    if constexpr (VEC) {
         // pairs of blocks trade halves between lane rows g and g ^ 1, so that a
         // lane holds 8 consecutive columns: one 16-byte store
         typedef unsigned short u16;
@@ -492,27 +502,13 @@ __global__ __launch_bounds__(256) void mxfp4_gemm_tile_kernel(const MxGemmParams
                 if (row + a * 16 < p.m && c8 + b * 16 < p.n)
                     *reinterpret_cast<u32x4 *>(c + (long long)a * 16 * p.n + b * 16) = v;
             }
-    } else if constexpr (VEC) {
-        float *c = reinterpret_cast<float *>(p.c) + row * p.n + col + 4 * g;
-        auto each = [&](auto add) __attribute__((always_inline)) {
-#pragma unroll
-            for (int a = 0; a < WB; ++a)
-#pragma unroll
-                for (int b = 0; b < WB; ++b)
-                    if (row + a * 16 < p.m && col + 4 * g + b * 16 < p.n) {
-                        f32x4 *at = reinterpret_cast<f32x4 *>(c + (long long)a * 16 * p.n + b * 16);
-                        *at = decltype(add)::value ? *at + acc[a][b] : acc[a][b];
-                    }
-        };
-        if (p.accumulate)
-            each(std::true_type{});
-        else
-            each(std::false_type{});
     } else {
 #pragma unroll
-        for (int a = 0; a < WB; ++a)
+        for (int a = 0; a < WB; ++a) {
 #pragma unroll
             for (int b = 0; b < WB; ++b) store_c<CT>(p, row + a * 16, col + b * 16 + 4 * g, acc[a][b]);
+            MX_FENCE();
+        }
     }
 #endif
 }
@@ -522,11 +518,14 @@ hipError_t launch_tile(const MxGemmParams &p, hipStream_t stream)
 {
     const int T = 32 * WB;
     const int tm = (int)((p.m + T - 1) / T), tn = (int)((p.n + T - 1) / T);
-    const bool vec = (uintptr_t)p.c % 16 == 0 && p.n % (CT == kBF16 ? 8 : 4) == 0;
-    if (vec)
-        mxfp4_gemm_tile_kernel<WB, CT, true><<<tm * tn, 256, 0, stream>>>(p, tm, tn);
-    else
-        mxfp4_gemm_tile_kernel<WB, CT, false><<<tm * tn, 256, 0, stream>>>(p, tm, tn);
+    if constexpr (CT == kBF16) {
+        // rows of C on 16 bytes: 16-byte stores
+        if ((uintptr_t)p.c % 16 == 0 && p.n % 8 == 0) {
+            mxfp4_gemm_tile_kernel<WB, CT, true><<<tm * tn, 256, 0, stream>>>(p, tm, tn);
+            return hipGetLastError();
+        }
+    }
+    mxfp4_gemm_tile_kernel<WB, CT, false><<<tm * tn, 256, 0, stream>>>(p, tm, tn);
     return hipGetLastError();
 }
 

@@ -57,7 +57,7 @@ def test_grad_norm_refusals():
     assert norm(ws=None) == INVALID and norm(ws=B[2] + 4) == INVALID
     assert norm(most=-1.0) == INVALID and norm(most=NAN) == INVALID and norm(most=INF) == INVALID
     assert norm(ctrl=B[2] + 16) == ALIAS
-    assert norm(g=B[1] - 396) == ALIAS and norm(g=B[2] + 16000) == ALIAS
+    assert norm(g=B[1] - 396) == ALIAS and norm(g=B[2] + T.GRAD_NORM_WS_BYTES - 4) == ALIAS
     assert dps.lib().dp_grad_norm(1, None, P([B[0]]), F32, 1.0, B[1], B[2], None) == INVALID
     assert dps.lib().dp_grad_norm(1, counts(1), None, F32, 1.0, B[1], B[2], None) == INVALID
 

@@ -1,0 +1,92 @@
+"""Properties of the gfx950 code that the optimizer and 4-bit kernels compile to
+(CPU only): no scratch, no packed fp32, wide accesses whatever the alignment,
+and, in the tiled product, accumulators that stay where they are, waits only
+where they are written, and matrix instructions of the 4-bit format."""
+import os
+import re
+import subprocess
+import tempfile
+
+import pytest
+
+from gradient_sync_amd import _build as B
+
+SOURCES = ["optim_kernels.hip", "mxfp4_quant.hip", "mxfp4_gemm.hip"]
+
+
+@pytest.fixture(scope="module")
+def kernels():
+    out = {}
+    with tempfile.TemporaryDirectory() as tmp:
+        procs = []
+        for src in SOURCES:
+            asm = os.path.join(tmp, src + ".s")
+            cmd = [B.HIPCC, *B.FLAGS, "-I", B.CSRC, "-I", os.path.join(B.ROOT, "include"), "--cuda-device-only", "-S",
+                   os.path.join(B.CSRC, src), "-o", asm]
+            procs.append((asm, subprocess.Popen(cmd, stdout=subprocess.DEVNULL, stderr=subprocess.DEVNULL)))
+        for asm, p in procs:
+            assert p.wait() == 0, asm
+            text = open(asm).read()
+            for m in re.finditer(r"\.amdhsa_kernel (\S+)(.*?)\.end_amdhsa_kernel", text, re.S):
+                start = re.search(r"^" + re.escape(m.group(1)) + r":", text, re.M).start()
+                out[m.group(1)] = (m.group(2), text[start:text.index(".Lfunc_end", start)])
+    return out
+
+
+def pick(kernels, part):
+    found = {n: v for n, v in kernels.items() if part in n}
+    assert found, part
+    return found
+
+
+def test_no_scratch_and_no_packed_fp32(kernels):
+    assert len(kernels) >= 28
+    for name, (desc, body) in kernels.items():
+        assert int(re.search(r"private_segment_fixed_size (\d+)", desc).group(1)) == 0, name
+        assert not re.search(r"\bv_pk_(add|mul|fma)_f32\b", body), name
+
+
+def test_wide_accesses(kernels):
+    for name, (_, body) in pick(kernels, "grad_norm_kernel").items():
+        assert re.search(r"global_load_dwordx4 .* nt", body), name
+    for name, (_, body) in pick(kernels, "adamw_kernelILi0ELi0ELb0").items():
+        assert len(re.findall(r"global_load_dwordx4 .* nt", body)) >= 8, name
+        assert len(re.findall(r"global_store_dwordx4 .* nt", body)) >= 6, name
+    for name, (_, body) in pick(kernels, "mxfp4_quantize").items():
+        assert "global_load_dwordx4" in body, name
+
+
+def test_the_norm_neither_writes_back_nor_drops_caches(kernels):
+    for name, (_, body) in pick(kernels, "grad_norm_kernel").items():
+        assert not re.search(r"\bbuffer_(wbl2|inv)\b", body), name
+
+
+def test_tiled_product_loop(kernels):
+    for name, (_, body) in pick(kernels, "mxfp4_gemm_tile_kernel").items():
+        lines = body.splitlines()
+        start = next(i for i, ln in enumerate(lines) if "Inner Loop Header" in ln)
+        label = re.match(r"(\.LBB\d+_\d+):", lines[start]).group(1)
+        end = max(i for i, ln in enumerate(lines) if re.search(r"s_cbranch\w* " + re.escape(label) + r"\b", ln))
+        loop = "\n".join(lines[start:end])
+        wb = 8 if "tile_kernelILi8" in name else 4
+        assert len(re.findall(r"v_mfma_scale_f32_16x16x128_f8f6f4 a\[", loop)) == 4 * wb * wb, name
+        assert loop.count("cbsz:4 blgp:4") == 4 * wb * wb, name
+        assert not re.search(r"\bv_accvgpr", loop), name
+        assert len(re.findall(r"\bs_barrier\b", loop)) == 4, name
+        assert len(re.findall(r"s_waitcnt vmcnt", loop)) == 4, name
+        # nothing but the choice of scale bytes between the matrix instructions
+        valu = {m for m in re.findall(r"^\s*(v_\w+)", loop, re.M) if not m.startswith("v_mfma")}
+        assert valu == {"v_perm_b32"}, (name, valu)
+
+
+def test_few_row_products_branch_by_scalars(kernels):
+    """A matrix instruction runs whatever the lane mask says: what skips one is a jump, not a mask."""
+    for name, (_, body) in pick(kernels, "mxfp4_gemm_few_kernel").items():
+        lines = body.splitlines()
+        for i, ln in enumerate(lines):
+            if "v_mfma" not in ln:
+                continue
+            for back in reversed(lines[:i]):
+                if re.match(r"\.LBB", back) or "v_mfma" in back or "s_cbranch" in back:
+                    break
+                assert "saveexec" not in back, name
