@@ -278,11 +278,11 @@ __device__ __forceinline__ void mfma_acc(f32x4 &c, u32x4 first, unsigned fs, u32
         MX_MFMA("op_sel:[1,1,0] op_sel_hi:[1,1,0]");
 #undef MX_MFMA
 }
-// until at most NEWER loads of this wave are on their way and none of its LDS reads
-template <int NEWER>
+// until at most NEWER loads of this wave are on their way and, with READS, none of its LDS reads
+template <int NEWER, bool READS>
 __device__ __forceinline__ void mx_wait()
 {
-    __builtin_amdgcn_s_waitcnt((NEWER & 15) | 0x70 | (NEWER >> 4 << 14));
+    __builtin_amdgcn_s_waitcnt((NEWER & 15) | 0x70 | (READS ? 0 : 0xF00) | (NEWER >> 4 << 14));
 }
 // names a value as one in a vector register at this point
 __device__ __forceinline__ void mx_pin(unsigned &x)
@@ -422,10 +422,12 @@ __global__ __launch_bounds__(256) void mxfp4_gemm_tile_kernel(const MxGemmParams
     // newer than the last one of B (of A) where it has to have landed:
     constexpr int kLoads = (N / 2 + DV - 1) / DV, kScales = (N / 2 + EV - 2) / EV;
     constexpr int kScalesAfterB = 2 * WB - (DV * (WB - 1) + EV - 1) / EV;
-    // waits until at most that many of this wave's loads are on their way and its LDS reads are done, then for the others
-    auto meet = [&](auto newer) __attribute__((always_inline)) {
+    // waits until at most that many of this wave's loads are on their way, then for
+    // the other waves. Before step 1 its reads of step 1's fragments have to be
+    // over too, as the next loads go where they read.
+    auto meet = [&](auto newer, auto reads) __attribute__((always_inline)) {
         MX_FENCE();
-        mx_wait<decltype(newer)::value>();
+        mx_wait<decltype(newer)::value, decltype(reads)::value>();
         __builtin_amdgcn_s_barrier();
         MX_FENCE();
     };
@@ -438,10 +440,10 @@ __global__ __launch_bounds__(256) void mxfp4_gemm_tile_kernel(const MxGemmParams
             mfma_acc<2 * buf>(acc[q / WB][q % WB], bf[0][q % WB], sb[q % WB], af[0][q / WB], sa[q / WB]);
             MX_FENCE();
         }
-        meet(std::integral_constant<int, WB + (buf == 1 ? kScalesAfterB : 0)>{});                        // B of stage t + 1 is there
+        meet(std::integral_constant<int, WB + (buf == 1 ? kScalesAfterB : 0)>{}, std::true_type{});                        // B of stage t + 1 is there
 #pragma unroll
         for (int q = 0; q < N; ++q) {
-            if (q == N / 2) meet(std::integral_constant<int, kLoads + (buf == 0 ? kScales : 0)>{});      // A of stage t + 1 is there
+            if (q == N / 2) meet(std::integral_constant<int, kLoads + (buf == 0 ? kScales : 0)>{}, std::false_type{});      // A of stage t + 1 is there
             if (q % EV == 0) rdq(0, buf ^ 1, 0, q / EV);
             if constexpr (buf == 0) {
                 if (q % EV == 1) ns[q / EV] = scale(q / EV, next_kt);
