@@ -253,9 +253,11 @@ __device__ __forceinline__ double power(double b, long long t)
     return r;
 }
 
-// n (1..4) elements at p[e]; FULL: all four, in one access
+// 4 elements at p[e] in one access (FULL), or the first n of them and zeros: every
+// load of a short chunk is issued, from the tensor's last element where there is
+// none, as a load behind a branch would be waited for before the next one
 template <int DT, bool FULL>
-__device__ __forceinline__ void load4(const char *p, long long e, int n, float (&x)[4])
+__device__ __forceinline__ void load4(const char *p, long long e, int n, long long last, float (&x)[4])
 {
     if constexpr (FULL && DT == kF32) {
         const f32x4 w = load_once(reinterpret_cast<const f32x4_e *>(p + 4 * e));
@@ -269,8 +271,11 @@ __device__ __forceinline__ void load4(const char *p, long long e, int n, float (
         x[3] = __uint_as_float(w[1] & 0xffff0000u);
     } else {
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-            x[i] = i >= n ? 0.0f : DT == kF32 ? reinterpret_cast<const float *>(p)[e + i] : bf16_at(p, e + i);
+        for (int i = 0; i < 4; ++i) {
+            const long long at = min(e + i, last);
+            const float v = DT == kF32 ? reinterpret_cast<const float *>(p)[at] : bf16_at(p, at);
+            x[i] = i < n ? v : 0.0f;
+        }
     }
 }
 
@@ -301,13 +306,15 @@ __device__ __forceinline__ void store4(char *p, long long e, int n, const float 
 }
 
 template <bool FULL>
-__device__ __forceinline__ unsigned load_codes(const char *p, long long e, int n)
+__device__ __forceinline__ unsigned load_codes(const char *p, long long e, int n, long long last)
 {
     if constexpr (FULL) return load_once(reinterpret_cast<const u32_e *>(p + e));
     unsigned w = 0;
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-        if (i < n) w |= (unsigned)(unsigned char)p[e + i] << (8 * i);
+    for (int i = 0; i < 4; ++i) {
+        const unsigned v = (unsigned char)p[min(e + i, last)];
+        w |= (i < n ? v : 0u) << (8 * i);
+    }
     return w;
 }
 
@@ -338,8 +345,12 @@ __device__ __forceinline__ Scalars scalars(const AdamParams &k)
             // as the host does it for a given step, in fp64 and rounded once: even
             // lanes lr / (1 - beta1^t), odd lanes 1 / sqrt(1 - beta2^t)
             c.step = max(1, k.ctrl->step);
+            double b1 = k.dbeta1, b2 = k.dbeta2;
+#ifdef __HIP_DEVICE_COMPILE__
+            asm volatile("" : "+s"(b1), "+s"(b2));    // scalars: chosen by address, they would wait for the loads above
+#endif
             const bool odd = threadIdx.x & 1;
-            const double left = 1.0 - power(odd ? k.dbeta2 : k.dbeta1, c.step);
+            const double left = 1.0 - power(odd ? b2 : b1, c.step);
             const int x = __float_as_int((float)((odd ? 1.0 : k.lr) / (odd ? sqrt(left) : left)));
             c.step_size = __int_as_float(__builtin_amdgcn_readlane(x, 0));
             c.inv_sqrt_bc2 = __int_as_float(__builtin_amdgcn_readlane(x, 1));
@@ -357,19 +368,20 @@ __device__ __forceinline__ void adam_chunk(const AdamParams &k, const AdamTensor
     f32x2 sc[kAdamU];
     long long e[kAdamU];
     int n[kAdamU];
+    const long long last = t.n - 1;
 #pragma unroll
     for (int u = 0; u < kAdamU; ++u) {
         e[u] = at + (u * kNT + (int)threadIdx.x) * 4;
         n[u] = FULL ? 4 : (int)max(0LL, min(4LL, t.n - e[u]));
-        load4<GT, FULL>(t.g, e[u], n[u], g[u]);
-        load4<PT, FULL>(t.p, e[u], n[u], p[u]);
+        load4<GT, FULL>(t.g, e[u], n[u], last, g[u]);
+        load4<PT, FULL>(t.p, e[u], n[u], last, p[u]);
         if constexpr (S8) {
-            mw[u] = load_codes<FULL>(t.m, e[u], n[u]);
-            vw[u] = load_codes<FULL>(t.v, e[u], n[u]);
-            sc[u] = n[u] > 0 ? reinterpret_cast<const f32x2 *>(t.scales)[e[u] / kStateBlock] : f32x2{0.0f, 0.0f};
+            mw[u] = load_codes<FULL>(t.m, e[u], n[u], last);
+            vw[u] = load_codes<FULL>(t.v, e[u], n[u], last);
+            sc[u] = reinterpret_cast<const f32x2 *>(t.scales)[min(e[u], last) / kStateBlock];
         } else {
-            load4<kF32, FULL>(t.m, e[u], n[u], m[u]);
-            load4<kF32, FULL>(t.v, e[u], n[u], v[u]);
+            load4<kF32, FULL>(t.m, e[u], n[u], last, m[u]);
+            load4<kF32, FULL>(t.v, e[u], n[u], last, v[u]);
         }
     }
     // after the loads have been issued: they take longer than this
