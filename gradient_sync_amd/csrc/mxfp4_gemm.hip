@@ -316,7 +316,13 @@ __device__ __forceinline__ void mx_settle() { asm volatile("s_nop 15\n\ts_nop 15
 // vanish against fp32's smallest 2^-149. One byte permutation with a scalar
 // selector does both. Rows past M or N are loads of the last row, and their
 // results are not stored.
-template <int WB, int CT, bool VEC>
+//
+// LOOP: a workgroup of the large tile has a CU to itself, so that nothing runs
+// while it starts and while it writes C. With more tiles than CUs, 256 workgroups
+// go through them instead, and load a tile's first stages during the last
+// ones of the tile before (8192 x 14336 x 4096: 211 us in place of 238; with one
+// tile a workgroup the loop around costs 2%).
+template <int WB, int CT, bool VEC, bool LOOP>
 __global__ __launch_bounds__(256) void mxfp4_gemm_tile_kernel(const MxGemmParams p, int tiles_m, int tiles_n)
 {
 #ifdef __HIP_DEVICE_COMPILE__                        // the host pass rejects the body's operands, and needs none
@@ -326,10 +332,6 @@ __global__ __launch_bounds__(256) void mxfp4_gemm_tile_kernel(const MxGemmParams
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int wi = wave >> 1, wj = wave & 1, i = lane & 15, g = lane >> 4;
-    int tm, tn;
-    tile_of(blockIdx.x, tiles_m, tiles_n, tm, tn);
-    const long long m0 = (long long)tm * T, n0 = (long long)tn * T;
-    const int rows_a = (int)min((long long)T, p.m - m0), rows_b = (int)min((long long)T, p.n - n0);
     const int pitch = (int)mx_pitch(p.k), ktiles = (int)mx_scale_tiles(p.k);
     const int steps = (int)((p.k + 127) / 128), pairs = (steps + 3) / 4;
     // selection of the last pair's scale bytes (see above; 0x0c selects a zero byte)
@@ -338,74 +340,83 @@ __global__ __launch_bounds__(256) void mxfp4_gemm_tile_kernel(const MxGemmParams
     auto abuf = [&](int buf) __attribute__((always_inline)) { return buf ? A1 : A0; };
     auto bbuf = [&](int buf) __attribute__((always_inline)) { return buf ? B1 : B0; };
 
-    // byte offsets within a tile's rows fit 31 bits (checked by the launcher)
-    const __amdgpu_buffer_rsrc_t rA =
-        __builtin_amdgcn_make_buffer_rsrc((void *)(p.a + m0 * pitch), (short)0, 0x7fffffff, 0x00020000);
-    const __amdgpu_buffer_rsrc_t rB =
-        __builtin_amdgcn_make_buffer_rsrc((void *)(p.b + n0 * pitch), (short)0, 0x7fffffff, 0x00020000);
-    const int lr = lane >> 3;
-    int off[2 * WB];
+    // the tile that is being loaded: its corner in C, and offsets within its
+    // rows of codes and scales, which fit 31 bits (checked by the launcher)
+    long long lm0, ln0;
+    const unsigned char *la, *lb, *lsa, *lsb;
+    int off[2 * WB], soff[2 * WB];
+    auto place = [&](int tile) __attribute__((always_inline)) {
+        int tm, tn;
+        tile_of(tile, tiles_m, tiles_n, tm, tn);
+        lm0 = (long long)tm * T;
+        ln0 = (long long)tn * T;
+        const int rows_a = (int)min((long long)T, p.m - lm0), rows_b = (int)min((long long)T, p.n - ln0);
+        la = p.a + lm0 * pitch;
+        lb = p.b + ln0 * pitch;
+        lsa = p.a_scales + lm0 / 16 * ktiles * 256;
+        lsb = p.b_scales + ln0 / 16 * ktiles * 256;
 #pragma unroll
-    for (int q = 0; q < 2 * WB; ++q) {
-        const int row = wave * 8 * WB + (q % WB) * 8 + lr;
-        off[q] = min(row, (q < WB ? rows_b : rows_a) - 1) * pitch + (((lane & 7) ^ lr) << 4);
-    }
+        for (int q = 0; q < 2 * WB; ++q) {
+            const int row = wave * 8 * WB + (q % WB) * 8 + (lane >> 3);
+            off[q] = min(row, (q < WB ? rows_b : rows_a) - 1) * pitch + (((lane & 7) ^ (lane >> 3)) << 4);
+        }
+#pragma unroll
+        for (int x = 0; x < WB; ++x) {
+            soff[x] = min(wi * WB + x, (rows_a - 1) >> 4) * ktiles * 256 + lane * 4;
+            soff[WB + x] = min(wj * WB + x, (rows_b - 1) >> 4) * ktiles * 256 + lane * 4;
+        }
+    };
+    auto rsrc = [](const unsigned char *base) __attribute__((always_inline)) {
+        return __builtin_amdgcn_make_buffer_rsrc((void *)base, (short)0, 0x7fffffff, 0x00020000);
+    };
     // a stage that reaches past the row is taken from the row's last 128 bytes
     auto dtl = [&](int buf, int stage, int q) __attribute__((always_inline)) {
         const int row0 = wave * 8 * WB + (q % WB) * 8;
         const int so = __builtin_amdgcn_readfirstlane(min(stage * 128, pitch - 128));
-        if (q < WB)
-            __builtin_amdgcn_raw_ptr_buffer_load_lds(rB, (lds_void *)(bbuf(buf) + row0 * 128), 16, off[q], so, 0, 0);
-        else
-            __builtin_amdgcn_raw_ptr_buffer_load_lds(rA, (lds_void *)(abuf(buf) + row0 * 128), 16, off[q], so, 0, 0);
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc(q < WB ? lb : la),
+                                                 (lds_void *)((q < WB ? bbuf(buf) : abuf(buf)) + row0 * 128), 16, off[q], so,
+                                                 0, 0);
     };
-    // scales of 16-row group x of this wave's rows of A or B, pair of stages kt
-    const long long ga = m0 / 16, gb = n0 / 16;
-    const __amdgpu_buffer_rsrc_t sA =
-        __builtin_amdgcn_make_buffer_rsrc((void *)(p.a_scales + ga * ktiles * 256), (short)0, 0x7fffffff, 0x00020000);
-    const __amdgpu_buffer_rsrc_t sB =
-        __builtin_amdgcn_make_buffer_rsrc((void *)(p.b_scales + gb * ktiles * 256), (short)0, 0x7fffffff, 0x00020000);
-    int soff[2 * WB];
-#pragma unroll
-    for (int x = 0; x < WB; ++x) {
-        soff[x] = min(wi * WB + x, (rows_a - 1) >> 4) * ktiles * 256 + lane * 4;
-        soff[WB + x] = min(wj * WB + x, (rows_b - 1) >> 4) * ktiles * 256 + lane * 4;
-    }
-    auto scale = [&](int x, int kt) __attribute__((always_inline)) {      // x < WB: A's group x, else B's x - WB
-        return (unsigned)__builtin_amdgcn_raw_buffer_load_b32(x < WB ? sA : sB, soff[x], kt * 256, 0);
+    // scales of 16-row group x of this wave's rows (x < WB: A's group x, else B's x - WB), pair of stages kt
+    auto scale = [&](int x, int kt) __attribute__((always_inline)) {
+        return (unsigned)__builtin_amdgcn_raw_buffer_load_b32(rsrc(x < WB ? lsa : lsb), soff[x], kt * 256, 0);
     };
 
     f32x4 acc[WB][WB];
+    auto clear = [&]() __attribute__((always_inline)) {
 #pragma unroll
-    for (int a = 0; a < WB; ++a)
+        for (int a = 0; a < WB; ++a)
 #pragma unroll
-        for (int b = 0; b < WB; ++b) {
-            acc[a][b] = f32x4{};
-            asm volatile("" : "+a"(acc[a][b]));
-        }
-    mx_settle();
+            for (int b = 0; b < WB; ++b) {
+                acc[a][b] = f32x4{};
+                asm volatile("" : "+a"(acc[a][b]));
+            }
+        mx_settle();
+    };
+    clear();
     u32x4 af[2][WB], bf[2][WB];
     unsigned sa[WB], sb[WB], ns[2 * WB];
 
-    const int last = 2 * pairs - 1;
+    int tile = blockIdx.x;
+    place(tile);
+    long long m0 = lm0, n0 = ln0;
 #pragma unroll
     for (int q = 0; q < 2 * WB; ++q) dtl(0, 0, q);
 #pragma unroll
     for (int q = 0; q < 2 * WB; ++q) dtl(1, 1, q);
-    const unsigned sel0 = pairs == 1 ? tail : 0x03020100u;
 #pragma unroll
-    for (int x = 0; x < WB; ++x) {
-        sa[x] = __builtin_amdgcn_perm(0u, scale(x, 0), sel0);
-        sb[x] = __builtin_amdgcn_perm(0u, scale(WB + x, 0), sel0);
-        mx_pin(sa[x]);
-        mx_pin(sb[x]);
-    }
-    mx_settle();
-
+    for (int x = 0; x < 2 * WB; ++x) ns[x] = scale(x, 0);
+    MX_FENCE();
     auto take = [&](unsigned &x, unsigned next, unsigned sel) __attribute__((always_inline)) {
         x = __builtin_amdgcn_perm(0u, next, sel);
         mx_pin(x);
     };
+#pragma unroll
+    for (int x = 0; x < WB; ++x) {
+        take(sa[x], ns[x], pairs == 1 ? tail : 0x03020100u);
+        take(sb[x], ns[WB + x], pairs == 1 ? tail : 0x03020100u);
+    }
+    mx_settle();
     // fragment read q of a step: q < WB B's block q, else A's block q - WB
     const int fp = i * 128, fx = lane & 7;
     auto rdq = [&](int set, int buf, int ks, int q) __attribute__((always_inline)) {
@@ -425,14 +436,19 @@ __global__ __launch_bounds__(256) void mxfp4_gemm_tile_kernel(const MxGemmParams
     // waits until at most that many of this wave's loads are on their way, then for
     // the other waves. Before step 1 its reads of step 1's fragments have to be
     // over too, as the next loads go where they read.
-    auto meet = [&](auto newer, auto reads) __attribute__((always_inline)) {
+    // kStores: stores of the tile before that may be on their way besides.
+    constexpr int kStores = LOOP && VEC ? N / 2 : 0;
+    auto meet = [&](auto newer, auto reads, bool stores) __attribute__((always_inline)) {
         MX_FENCE();
-        mx_wait<decltype(newer)::value, decltype(reads)::value>();
+        if (kStores && stores)
+            mx_wait<decltype(newer)::value + kStores, decltype(reads)::value>();
+        else
+            mx_wait<decltype(newer)::value, decltype(reads)::value>();
         __builtin_amdgcn_s_barrier();
         MX_FENCE();
     };
     // stage 2 kt + buf; `next`: the stage to load two ahead, `sel`: the next pair's selection of scale bytes
-    auto stage = [&](auto buf_, int next, int next_kt, unsigned sel) __attribute__((always_inline)) {
+    auto stage = [&](auto buf_, int next, int next_kt, unsigned sel, bool stores) __attribute__((always_inline)) {
         constexpr int buf = decltype(buf_)::value;
 #pragma unroll
         for (int q = 0; q < N; ++q) {
@@ -440,10 +456,12 @@ __global__ __launch_bounds__(256) void mxfp4_gemm_tile_kernel(const MxGemmParams
             mfma_acc<2 * buf>(acc[q / WB][q % WB], bf[0][q % WB], sb[q % WB], af[0][q / WB], sa[q / WB]);
             MX_FENCE();
         }
-        meet(std::integral_constant<int, WB + (buf == 1 ? kScalesAfterB : 0)>{}, std::true_type{});                        // B of stage t + 1 is there
+        // B of stage t + 1 is there
+        meet(std::integral_constant<int, WB + (buf == 1 ? kScalesAfterB : 0)>{}, std::true_type{}, buf == 0 && stores);
 #pragma unroll
         for (int q = 0; q < N; ++q) {
-            if (q == N / 2) meet(std::integral_constant<int, kLoads + (buf == 0 ? kScales : 0)>{}, std::false_type{});      // A of stage t + 1 is there
+            if (q == N / 2)                          // A of stage t + 1 is there
+                meet(std::integral_constant<int, kLoads + (buf == 0 ? kScales : 0)>{}, std::false_type{}, buf == 0 && stores);
             if (q % EV == 0) rdq(0, buf ^ 1, 0, q / EV);
             if constexpr (buf == 0) {
                 if (q % EV == 1) ns[q / EV] = scale(q / EV, next_kt);
@@ -468,49 +486,70 @@ __global__ __launch_bounds__(256) void mxfp4_gemm_tile_kernel(const MxGemmParams
 #pragma unroll
     for (int q = 0; q < 2 * WB; ++q) rdq(0, 0, 0, q);
     MX_FENCE();
-    for (int kt = 0; kt < pairs; ++kt) {
-        // past the end the loads repeat the last stage into a buffer that is not read again
-        stage(std::integral_constant<int, 0>{}, min(2 * kt + 2, last), min(kt + 1, pairs - 1), 0u);
-        stage(std::integral_constant<int, 1>{}, min(2 * kt + 3, last), 0, kt + 2 == pairs ? tail : 0x03020100u);
-    }
-    __builtin_amdgcn_s_waitcnt(0x0F70);   // no load may land in LDS that is another workgroup's
-    mx_settle();
-#pragma unroll
-    for (int a = 0; a < WB; ++a)
-#pragma unroll
-        for (int b = 0; b < WB; ++b) asm volatile("" : "+a"(acc[a][b]));
-
     // C: lane (i, g) holds columns 4 g .. 4 g + 3 of row i of each block
-    const long long row = m0 + wi * 16 * WB + i, col = n0 + wj * 16 * WB;
-    if constexpr (VEC) {
-        // pairs of blocks trade halves between lane rows g and g ^ 1, so that a
-        // lane holds 8 consecutive columns: one 16-byte store
-        typedef unsigned short u16;
-        const long long c8 = col + 16 * (g & 1) + 8 * (g >> 1);
-        u16 *c = reinterpret_cast<u16 *>(p.c) + row * p.n + c8;
+    auto put = [&](long long m0, long long n0) __attribute__((always_inline)) {
+        const long long row = m0 + wi * 16 * WB + i, col = n0 + wj * 16 * WB;
+        if constexpr (VEC) {
+            // pairs of blocks trade halves between lane rows g and g ^ 1, so that a
+            // lane holds 8 consecutive columns: one 16-byte store
+            typedef unsigned short u16;
+            const long long c8 = col + 16 * (g & 1) + 8 * (g >> 1);
+            u16 *c = reinterpret_cast<u16 *>(p.c) + row * p.n + c8;
+#pragma unroll
+            for (int a = 0; a < WB; ++a)
+#pragma unroll
+                for (int b = 0; b < WB; b += 2) {
+                    const f32x4 x = acc[a][b], y = acc[a][b + 1];
+                    const mx_f32x2 x0 = {x[0], x[1]}, x1 = {x[2], x[3]}, y0 = {y[0], y[1]}, y1 = {y[2], y[3]};
+                    const auto s0 = __builtin_amdgcn_permlane16_swap(
+                        __builtin_bit_cast(unsigned, __builtin_convertvector(x0, mx_bf16x2)),
+                        __builtin_bit_cast(unsigned, __builtin_convertvector(y0, mx_bf16x2)), false, false);
+                    const auto s1 = __builtin_amdgcn_permlane16_swap(
+                        __builtin_bit_cast(unsigned, __builtin_convertvector(x1, mx_bf16x2)),
+                        __builtin_bit_cast(unsigned, __builtin_convertvector(y1, mx_bf16x2)), false, false);
+                    const u32x4 v = {s0[0], s1[0], s0[1], s1[1]};
+                    if (row + a * 16 < p.m && c8 + b * 16 < p.n)
+                        *reinterpret_cast<u32x4 *>(c + (long long)a * 16 * p.n + b * 16) = v;
+                }
+        } else {
+#pragma unroll
+            for (int a = 0; a < WB; ++a) {
+#pragma unroll
+                for (int b = 0; b < WB; ++b) store_c<CT>(p, row + a * 16, col + b * 16 + 4 * g, acc[a][b]);
+                MX_FENCE();
+            }
+        }
+    };
+    const int tiles = tiles_m * tiles_n;
+    bool stores = false;
+    for (;;) {
+        const int following = tile + gridDim.x;
+        for (int kt = 0; kt < pairs; ++kt) {
+            // the last pair loads the first pair of the workgroup's next tile, whose
+            // first stage then goes on without a pause (without a next tile, this
+            // one's again, to be read by no one)
+            const int next = kt + 1 < pairs ? kt + 1 : 0;
+            if (LOOP && next == 0 && following < tiles) place(following);
+            stage(std::integral_constant<int, 0>{}, 2 * next, next, 0u, stores);
+            stage(std::integral_constant<int, 1>{}, 2 * next + 1, 0, next + 1 == pairs ? tail : 0x03020100u, false);
+            stores = false;
+        }
+        // the last loads land before the workgroup ends, and its LDS is another's
+        const bool done = !LOOP || following >= tiles;
+        if (done) __builtin_amdgcn_s_waitcnt(0x0F70);
+        mx_settle();
 #pragma unroll
         for (int a = 0; a < WB; ++a)
 #pragma unroll
-            for (int b = 0; b < WB; b += 2) {
-                const f32x4 x = acc[a][b], y = acc[a][b + 1];
-                const mx_f32x2 x0 = {x[0], x[1]}, x1 = {x[2], x[3]}, y0 = {y[0], y[1]}, y1 = {y[2], y[3]};
-                const auto s0 = __builtin_amdgcn_permlane16_swap(
-                    __builtin_bit_cast(unsigned, __builtin_convertvector(x0, mx_bf16x2)),
-                    __builtin_bit_cast(unsigned, __builtin_convertvector(y0, mx_bf16x2)), false, false);
-                const auto s1 = __builtin_amdgcn_permlane16_swap(
-                    __builtin_bit_cast(unsigned, __builtin_convertvector(x1, mx_bf16x2)),
-                    __builtin_bit_cast(unsigned, __builtin_convertvector(y1, mx_bf16x2)), false, false);
-                const u32x4 v = {s0[0], s1[0], s0[1], s1[1]};
-                if (row + a * 16 < p.m && c8 + b * 16 < p.n)
-                    *reinterpret_cast<u32x4 *>(c + (long long)a * 16 * p.n + b * 16) = v;
-            }
-    } else {
-#pragma unroll
-        for (int a = 0; a < WB; ++a) {
-#pragma unroll
-            for (int b = 0; b < WB; ++b) store_c<CT>(p, row + a * 16, col + b * 16 + 4 * g, acc[a][b]);
-            MX_FENCE();
-        }
+            for (int b = 0; b < WB; ++b) asm volatile("" : "+a"(acc[a][b]));
+        put(m0, n0);
+        if (done) return;
+        // a whole tile's stores are counted; of one at the edge of C some are not made
+        stores = m0 + T <= p.m && n0 + T <= p.n;
+        tile = following;
+        m0 = lm0;
+        n0 = ln0;
+        clear();
     }
 #endif
 }
@@ -520,14 +559,23 @@ hipError_t launch_tile(const MxGemmParams &p, hipStream_t stream)
 {
     const int T = 32 * WB;
     const int tm = (int)((p.m + T - 1) / T), tn = (int)((p.n + T - 1) / T);
+    constexpr int CUS = 256;
+    const bool loop = WB == 8 && tm * tn > CUS;
+    const int grid = loop ? CUS : tm * tn;
     if constexpr (CT == kBF16) {
         // rows of C on 16 bytes: 16-byte stores
         if ((uintptr_t)p.c % 16 == 0 && p.n % 8 == 0) {
-            mxfp4_gemm_tile_kernel<WB, CT, true><<<tm * tn, 256, 0, stream>>>(p, tm, tn);
+            if (loop)
+                mxfp4_gemm_tile_kernel<WB, CT, true, WB == 8><<<grid, 256, 0, stream>>>(p, tm, tn);
+            else
+                mxfp4_gemm_tile_kernel<WB, CT, true, false><<<grid, 256, 0, stream>>>(p, tm, tn);
             return hipGetLastError();
         }
     }
-    mxfp4_gemm_tile_kernel<WB, CT, false><<<tm * tn, 256, 0, stream>>>(p, tm, tn);
+    if (loop)
+        mxfp4_gemm_tile_kernel<WB, CT, false, WB == 8><<<grid, 256, 0, stream>>>(p, tm, tn);
+    else
+        mxfp4_gemm_tile_kernel<WB, CT, false, false><<<grid, 256, 0, stream>>>(p, tm, tn);
     return hipGetLastError();
 }
 
