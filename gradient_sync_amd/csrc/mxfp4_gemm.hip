@@ -586,19 +586,22 @@ hipError_t launch_typed(const MxGemmParams &p, int x_dt, hipStream_t stream)
     if (p.m <= 32) return launch_few<2, CT>(p, x_dt, stream);
     // the tiled kernels need rows of 128 bytes, and offsets within a tile of 31 bits
     if (p.k <= 128 || mx_pitch(p.k) * 260 > 0x7fffffffLL) return launch_few<4, CT>(p, x_dt, stream);
-    // Microseconds, fitted to 40 shapes (m 33 .. 8192, n 1000 .. 14336, k 2000 ..
-    // 14336; each within a fifth of the measured times):
+    // Microseconds, fitted to 50 shapes (m 33 .. 8192, n 1000 .. 14336, k 512 ..
+    // 14336), most within a tenth of what was measured:
     // few rows: 80 rows of codes per workgroup, one at 35 GB/s, all at 8.3 TB/s;
-    // tiles of 128: a stage of 256 takes a lone workgroup 0.42, and a CU with
-    //   several 0.62 each;
-    // tiles of 256: one workgroup a CU, 1.8 a stage and 5.5 to begin and end.
+    // tiles of 128: a stage of 256 takes a lone workgroup 0.45, and 256 of them
+    //   together 0.44 and 2.2 to begin and end;
+    // tiles of 256: a stage takes 1.65, a tile's beginning and end 6.
+    // Where they differ most: 64 x 14336 x 4096 few 21.9, 128 11.4; 256 x 1000 x
+    // 2000 few 5.5, 128 6.9; 8192 x 8192 x 4096 128 152, 256 130; 4300 x 4400 x
+    // 640 128 22.4, 256 26.5.
     const double k = (double)p.k, stages = k / 256;
     const double few = (double)((p.m + 63) / 64) * (double)((p.n + 15) / 16);
     const double t128 = (double)((p.m + 127) / 128) * (double)((p.n + 127) / 128);
     const double t256 = (double)((p.m + 255) / 256) * (double)((p.n + 255) / 256);
     const double us_few = 2.0 + std::max(k * 1.16e-3, few * 40.0 * k / 8.3e6);
-    const double us_128 = 3.5 + stages * std::max(0.42, 0.62 * t128 / 256);
-    const double us_256 = std::ceil(t256 / 256) * (5.5 + 1.8 * stages);
+    const double us_128 = 3.0 + std::max(1.0 + 0.45 * stages, t128 / 256 * (2.2 + 0.44 * stages));
+    const double us_256 = 3.0 + std::ceil(t256 / 256) * (6.0 + 1.65 * stages);
     if (us_few <= us_128 && us_few <= us_256) return launch_few<4, CT>(p, x_dt, stream);
     return us_128 <= us_256 ? launch_tile<4, CT>(p, stream) : launch_tile<8, CT>(p, stream);
 }

@@ -215,16 +215,22 @@ def test_product_is_exact_for_small_integers(m, n, k):
 
 
 @pytest.mark.parametrize("dtype", [F32, BF16])
-@pytest.mark.parametrize("m,n,k", [(4096, 2560, 512), (4001, 2500, 1100), (3900, 2601, 640), (2561, 4090, 130)])
+@pytest.mark.parametrize("m,n,k", [(4096, 2560, 512), (4001, 2500, 1100), (3900, 2601, 640), (2561, 4090, 130),
+                                   (4096, 4096, 1024), (4001, 4090, 1100), (8192, 8192, 200), (8000, 5000, 1400),
+                                   (7941, 5099, 1400)])
 def test_product_of_large_matrices(m, n, k, dtype):
-    """Enough of C for the large tile, with and without edges, rows of C on 16 bytes or not."""
+    """Enough of C for the large tile, one a workgroup or several in turn, with and without edges, rows of C
+    on 16 bytes or not."""
     a, b = dps.dp_mxfp4_quantize(rand((m, k), 1)), dps.dp_mxfp4_quantize(rand((n, k), 2))
     buf = torch.full((m * n + 64,), 5.0, dtype=dtype, device=DEV)
     out = buf[32:32 + m * n].view(m, n)
     say("large product", m, n, k, dtype)
     dps.dp_gemm_mxfp4(a, b, out=out)
     first = out.clone()
-    check_product(out, values(a), values(b), dtype=dtype)
+    va, vb = (dps.dp_mxfp4_dequantize(q, dtype=F32).double() for q in (a, b))
+    want, mag = va @ vb.t().contiguous(), va.abs() @ vb.abs().t().contiguous()
+    tol = k * 2.0 ** -23 * mag + (2.0 ** -8 * want.abs() if dtype == BF16 else 0)
+    assert bool(((out.double() - want).abs() <= tol).all())
     if dtype == F32:
         dps.dp_gemm_mxfp4(a, b, out=out, accumulate=True)
         assert torch.equal(out, first + first)
