@@ -219,11 +219,12 @@ constexpr unsigned long long kGolden = 0x9E3779B97F4A7C15ull;
 // e4m3 keeps 3 of fp32's 23 fraction bits, so from its lowest octave up that is
 // an addition to the other 20 and a mask; a value below 2^-6 is first moved into
 // that octave, where u is the same. 448 has none of those 20 bits, and no more than
-// a few of them set for a rounding above it: nothing is carried past 448.
+// a few of them set for a rounding above it: nothing is carried past 448. A NaN is
+// brought to the lowest quiet one first, so that the addition leaves it a NaN.
 __device__ __forceinline__ float e4m3_stochastic(float y, unsigned r16)
 {
     const float a = fabsf(y), move = a < 0x1p-6f ? 0x1p-6f : 0.0f;
-    const unsigned bits = (__float_as_uint(a + move) + (r16 << 4)) & 0xfff00000u;
+    const unsigned bits = (min(__float_as_uint(a + move), 0x7fc00000u) + (r16 << 4)) & 0xfff00000u;
     return copysignf(__uint_as_float(bits) - move, y);
 }
 

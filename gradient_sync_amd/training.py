@@ -64,10 +64,10 @@ def _on(stream):
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
-def _at(stream, t):
-    """The handle of `stream`, or of the current stream of t's GPU."""
+def _at(stream):
+    """The handle of `stream`, or of the current stream."""
     if stream is None and _raw_stream is not None:
-        return _raw_stream(t.get_device())
+        return _raw_stream(torch.cuda.current_device())
     return _stream(stream)
 
 
@@ -107,8 +107,7 @@ class GradNorm:
 
     def run(self, max_norm: float = 0.0, stream=None) -> StepCtrl:
         _check(lib().dp_grad_norm(*self._args, float(max_norm), self.ctrl.buf.data_ptr(),
-                                  self.workspace.data_ptr(), _at(stream, self.workspace)),
-               "dp_grad_norm")
+                                  self.workspace.data_ptr(), _at(stream)), "dp_grad_norm")
         return self.ctrl
 
 
@@ -176,13 +175,12 @@ class AdamW:
              stream=None):
         """One update. step: its number (from 1); 0 takes it from ctrl, which
         also gives the clip factor."""
-        g = self.tensors[1]
         self.opts.step = step
         if lr is not None:
             self.opts.lr = lr
         _check(getattr(lib(), self._name)(*self._args, ctypes.byref(self.opts),
                                           None if ctrl is None else ctrl.buf.data_ptr(),
-                                          _at(stream, g[0]) if g else _stream(stream)), self._name)
+                                          _at(stream)), self._name)
 
 
 def dp_grad_norm(grads, ctrl: StepCtrl | None = None, max_norm: float = 0.0, stream=None) -> StepCtrl:
@@ -272,7 +270,7 @@ def dp_mxfp4_quantize(x, transposed: str = "no", out: Mxfp4 | None = None,
             raise ValueError("dp_mxfp4_quantize: out_t has another shape than x's transpose")
         ptrs[2:] = out_t.codes.data_ptr(), out_t.scales.data_ptr()
     _check(lib().dp_mxfp4_quantize(x.data_ptr(), rows, cols, ld, _DTYPES[x.dtype], *ptrs,
-                                   _at(stream, x)), "dp_mxfp4_quantize")
+                                   _at(stream)), "dp_mxfp4_quantize")
     return (out, out_t) if transposed == "also" else out if out is not None else out_t
 
 
@@ -280,7 +278,7 @@ def dp_mxfp4_dequantize(q: Mxfp4, out=None, dtype=torch.bfloat16, stream=None):
     """The values `q` stands for (exact)."""
     out = _output(out, (q.rows, q.cols), dtype, q.codes, stream, "out")
     _check(lib().dp_mxfp4_dequantize(q.codes.data_ptr(), q.scales.data_ptr(), q.rows, q.cols,
-                                     out.data_ptr(), q.cols, _DTYPES[out.dtype], _at(stream, out)),
+                                     out.data_ptr(), q.cols, _DTYPES[out.dtype], _at(stream)),
            "dp_mxfp4_dequantize")
     return out
 
@@ -296,7 +294,7 @@ def dp_gemm_mxfp4(a: Mxfp4, b: Mxfp4, out=None, dtype=torch.bfloat16, accumulate
     out = _output(out, (a.rows, b.rows), dtype, a.codes, stream, "out")
     _check(lib().dp_gemm_mxfp4(a.codes.data_ptr(), a.scales.data_ptr(), b.codes.data_ptr(),
                                b.scales.data_ptr(), out.data_ptr(), a.rows, b.rows, a.cols,
-                               _DTYPES[out.dtype], 1 if accumulate else 0, _at(stream, out)),
+                               _DTYPES[out.dtype], 1 if accumulate else 0, _at(stream)),
            "dp_gemm_mxfp4")
     return out
 
@@ -312,5 +310,5 @@ def dp_mxfp4_linear(x, w: Mxfp4, out=None, dtype=torch.bfloat16, stream=None):
     _check(lib().dp_mxfp4_linear(x.data_ptr(), ldx, _DTYPES[x.dtype], w.codes.data_ptr(),
                                  w.scales.data_ptr(), out.data_ptr(), m, w.rows, k,
                                  _DTYPES[out.dtype], ws.data_ptr() if need else None,
-                                 _at(stream, x)), "dp_mxfp4_linear")
+                                 _at(stream)), "dp_mxfp4_linear")
     return out

@@ -505,7 +505,8 @@ dp_status_t dp_adamw(int nt, const int64_t *counts, void *const *params, int p_d
  * codes, where that largest value is below 2^-100). A positive sqrt(v) is
  * never held as zero but at least as the smallest code. The parameters are
  * updated from the new m and v before these are rounded. All-zero
- * codes and scales are the initial state.
+ * codes and scales are the initial state. Without ctrl a NaN gradient leaves its
+ * element's states NaN, and an infinite one its block's.
  *   Rounding: to nearest even; with DP_ADAMW_STOCHASTIC to one of the two
  *   neighbours, with probability in proportion, from 16 bits r of a
  *   counter-based generator: |y| -> floor(|y| / u + r / 65536) u, u the step
@@ -537,7 +538,9 @@ dp_status_t dp_adamw8(int nt, const int64_t *counts, void *const *params, int p_
  *            blocks, 4-byte aligned; row r, block b at byte
  *            ((r / 16) * ceil(cols / 512) + b / 16) * 256
  *            + (16 (b % 4) + r % 16) * 4 + (b % 16) / 4
- *            (bytes of rows or blocks that do not exist are unspecified)
+ *            The blocks from cols up to a multiple of 128 have codes of zero and
+ *            any scale byte but 255 (dp_mxfp4_quantize writes 0); other bytes
+ *            of rows or blocks that do not exist are unspecified.
  * Row shards of a multiple of 16 rows are contiguous in both, so dp_all_gather
  * collects a quantised weight (as DP_I32: both sizes are multiples of 4).
  */

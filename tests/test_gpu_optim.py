@@ -304,6 +304,25 @@ def test_no_state_of_a_zero_block_is_lost_or_invented():
     assert not bool(m[0].any()) and bool(torch.isfinite(s[0]).all()) and bool(torch.isfinite(p[0]).all())
 
 
+@pytest.mark.parametrize("seed", [None, 4])
+def test_non_finite_gradients_without_a_control_block(seed):
+    """NaNs of any payload stay with their element, an infinity spoils its block, and no other block."""
+    n = 128 * 6
+    g = torch.full((n,), 0.25, device=DEV)
+    bits = g.view(torch.int32)
+    bits[3], bits[130], bits[131] = 0x7FFFFFFF, 0x7FC00000, -1
+    g[400] = float("inf")
+    p = [torch.zeros(n, device=DEV)]
+    m, v, s = dps.AdamW.new_state(p, 8)
+    dps.dp_adamw(p, [g], m, v, step=1, scales=s, lr=LR, seed=seed)
+    bad = torch.zeros(n, dtype=torch.bool, device=DEV)
+    bad[3] = bad[130] = bad[131] = bad[384:512] = True
+    for at, x in ((0, m[0]), (1, v[0])):
+        assert torch.equal(held(x, s[0], at).isnan(), bad)
+    bad[384:512] = False
+    assert torch.equal(p[0].isnan() | (torch.arange(n, device=DEV) == 400), bad | (torch.arange(n, device=DEV) == 400))
+
+
 def test_the_step_in_a_graph():
     """Norm and update captured once; each replay counts its step on the device and equals the eager call."""
     def make():
