@@ -502,8 +502,12 @@ template <int PT, int GT>
 hipError_t launch_adamw_typed(const AdamParams &p, bool eight, bool stochastic, hipStream_t stream)
 {
     const int grid = p.first[p.nt];
+    // fp32 states: LDS that the kernel does not use keeps a CU at two workgroups,
+    // 14 KiB a wave on their way, and their streams apart (200M elements: 977 us
+    // for 1051 with eight; three to five 1006-1018). With 8-bit states a wave
+    // computes longer and every one helps (578 us for 722).
     if (!eight)
-        adamw_kernel<PT, GT, false, false><<<grid, kNT, 0, stream>>>(p);
+        adamw_kernel<PT, GT, false, false><<<grid, kNT, 80 << 10, stream>>>(p);
     else if (!stochastic)
         adamw_kernel<PT, GT, true, false><<<grid, kNT, 0, stream>>>(p);
     else
