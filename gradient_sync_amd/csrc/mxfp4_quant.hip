@@ -68,7 +68,7 @@ __device__ __forceinline__ unsigned row_codes(const unsigned (&w)[In<DT>::W], un
 // Along the rows alone: a workgroup takes 16 rows by 512 columns, one tile of
 // scales, a wave 4 of the rows. A row is 1 KiB (bf16) of consecutive loads and
 // 256 bytes of codes; the tile's 256 scale bytes are put in order in LDS and
-// leave in one store.
+// leave in one store. HBM-bound: 8192 x 4096 bf16 in 15.5 us (5.5 TB/s).
 template <int DT>
 __global__ __launch_bounds__(kNT) void mxfp4_quantize_rows_kernel(const MxQuantParams p, int tiles)
 {
@@ -95,7 +95,9 @@ __global__ __launch_bounds__(kNT) void mxfp4_quantize_rows_kernel(const MxQuantP
 
 // Along the columns, and along the rows too with ROW: a workgroup reads a tile of
 // 128 x 128, quantises its rows from registers, and its columns from LDS, a
-// thread 32 rows of two neighbouring columns.
+// thread 32 rows of two neighbouring columns. HBM-bound, with 9% more written
+// than needed (scale bytes leave one by one): 14336 x 4096 bf16 both ways in
+// 37.8 us (4.75 TB/s).
 template <int DT, bool ROW>
 __global__ __launch_bounds__(kNT) void mxfp4_quantize_cols_kernel(const MxQuantParams p, int tiles_c)
 {
@@ -178,7 +180,8 @@ __global__ __launch_bounds__(kNT) void mxfp4_quantize_cols_kernel(const MxQuantP
     }
 }
 
-// One thread expands 8 codes (half of them for an odd tail).
+// One thread expands 8 codes, fewer at a row's end. HBM-bound: 14336 x 4096 to
+// bf16 in 24.2 us (6.1 TB/s).
 template <int DT>
 __global__ __launch_bounds__(kNT) void mxfp4_dequantize_kernel(const MxExpandParams p, long long groups)
 {

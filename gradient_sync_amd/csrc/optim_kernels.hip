@@ -53,6 +53,8 @@ __device__ __forceinline__ float bf16_at(const char *p, long long i)
 // overflows, and 10^9 terms lose nothing. Each thread holds four sums; a
 // workgroup's sum is a fixed tree over its threads, and the last workgroup to
 // finish adds the partials in a fixed order: the same bits in every run.
+// Bound by reading the gradients: 200M bf16 values in 62 us (6.45 TB/s), 10M
+// fp32 values in 12.5 (3.2 TB/s, the launch and the finish being half of it).
 constexpr int kNormChunk = 8192;
 
 template <int DT>
@@ -187,6 +189,12 @@ __global__ __launch_bounds__(kNT) void grad_norm_kernel(const NormParams p)
 // remainder: with b2 near 1 a moment changes by less than half a code per
 // step, and to nearest it would stand still relative to its block. 32 lanes of
 // a wave hold one block, so the two maxima are register exchanges.
+//
+// Bound by HBM: 200M elements in 64 shards (fp32 p, bf16 g and copy) take 1011
+// us with fp32 states (5.54 TB/s) and 617 with 8-bit ones, stochastically rounded
+// (5.22 TB/s); with bf16 p and stochastic rounding the vector units bound it
+// (460 us, 4.4 TB/s). One chunk per workgroup: workgroups that go through
+// several load nothing while they compute and store (1245 us against 1005).
 constexpr int kAdamU = 2;                        // groups of 4 elements per thread and chunk
 constexpr int kAdamChunk = kNT * 4 * kAdamU;
 

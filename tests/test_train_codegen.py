@@ -80,6 +80,15 @@ def test_tiled_product_loop(kernels):
             assert valu == {"v_perm_b32"}, (name, valu)
 
 
+def test_counted_stores(kernels):
+    """The kernel that goes through several tiles counts its stores of the tile before where it waits for
+    loads: 32 of them, and no other access to memory than the loads it counts."""
+    for name, (_, body) in pick(kernels, "mxfp4_gemm_tile_kernelILi8ELi1ELb1ELb1E").items():
+        assert len(re.findall(r"\bglobal_store_dwordx4\b", body)) == 32, name
+        assert not re.search(r"\b(global_load|flat_|scratch_|global_atomic)", body), name
+        assert len(re.findall(r"\bglobal_store", body)) == 32, name
+
+
 def test_few_row_products_branch_by_scalars(kernels):
     """A matrix instruction runs whatever the lane mask says: what skips one is a jump, not a mask."""
     for name, (_, body) in pick(kernels, "mxfp4_gemm_few_kernel").items():
