@@ -252,6 +252,20 @@ __device__ __forceinline__ void unpack_e4m3(unsigned w, float (&x)[4])
     x[3] = hi[1];
 }
 
+// sqrt(x) rounded to nearest: the hardware's root is off by at most one place, and
+// the sign of x - s (s -+ one place) tells. (The compiler's sqrtf also scales
+// arguments below 2^-96, where the residual loses digits; here such a root may
+// keep the hardware's error.) Zeros, infinities and NaNs pass through, as their
+// neighbours give NaN residuals.
+__device__ __forceinline__ float root(float x)
+{
+    const float s = __builtin_amdgcn_sqrtf(x);
+    const float down = __uint_as_float(__float_as_uint(s) - 1u), up = __uint_as_float(__float_as_uint(s) + 1u);
+    const float rd = __builtin_fmaf(-down, s, x), ru = __builtin_fmaf(-up, s, x);
+    const float t = rd <= 0.0f ? down : s;
+    return ru > 0.0f ? up : t;
+}
+
 __device__ __forceinline__ double power(double b, long long t)
 {
     double r = 1.0;
@@ -415,7 +429,7 @@ __device__ __forceinline__ void adam_chunk(const AdamParams &k, const AdamTensor
             const float gi = g[u][i] * c.clip;
             m[u][i] = m[u][i] * k.beta1 + gi * k.one_minus_beta1;
             v[u][i] = v[u][i] * k.beta2 + (gi * gi) * k.one_minus_beta2;
-            r[u][i] = sqrtf(v[u][i]);
+            r[u][i] = root(v[u][i]);
             // a hardware reciprocal (1 ulp) in place of a division: it enters the
             // parameter alone, at 2^-23 of the update. A denominator below
             // the normal numbers, whose reciprocal could overflow, counts as 2^-126
