@@ -214,7 +214,7 @@ def lib():
         L.dp_gemm_mxfp4.restype = _int
         L.dp_gemm_mxfp4.argtypes = [_vp] * 5 + [_i64, _i64, _i64, _int, _int, _vp]
         L.dp_mxfp4_linear_ws_bytes.restype = _sz
-        L.dp_mxfp4_linear_ws_bytes.argtypes = [_i64, _i64]
+        L.dp_mxfp4_linear_ws_bytes.argtypes = [_i64, _i64, _i64]
         L.dp_mxfp4_linear.restype = _int
         L.dp_mxfp4_linear.argtypes = [_vp, _i64, _int, _vp, _vp, _vp, _i64, _i64, _i64, _int, _vp,
                                       _vp]

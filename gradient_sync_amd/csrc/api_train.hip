@@ -324,9 +324,9 @@ dp_status_t dp_gemm_mxfp4(const void *a, const void *a_scales, const void *b, co
     return (dp_status_t)dps::hip_failure_code(e);
 }
 
-size_t dp_mxfp4_linear_ws_bytes(int64_t m, int64_t kk)
+size_t dp_mxfp4_linear_ws_bytes(int64_t m, int64_t n, int64_t kk)
 {
-    if (!mx_dims_ok(m, kk) || m <= dps::kMxFewRows) return 0;
+    if (!mx_dims_ok(m, kk) || !mx_dims_ok(m, n) || dps::mx_quantize_inside(m, n, kk)) return 0;
     return (dp_mxfp4_code_bytes(m, kk) + 255) / 256 * 256 + dp_mxfp4_scale_bytes(m, kk);
 }
 
@@ -339,7 +339,7 @@ dp_status_t dp_mxfp4_linear(const void *x, int64_t ldx, int x_dt, const void *w,
     if (!float_dt(x_dt) || !float_dt(y_dt)) return DP_ERR_UNSUPPORTED;
     if (m == 0 || n == 0) return DP_OK;
     const int xe = dps::elem_size(x_dt), ye = dps::elem_size(y_dt);
-    const size_t ws = dp_mxfp4_linear_ws_bytes(m, kk);
+    const size_t ws = dp_mxfp4_linear_ws_bytes(m, n, kk);
     if (!aligned(x, (uintptr_t)xe) || !mx_operand_ok(w, w_scales) || !aligned(y, (uintptr_t)ye) ||
         (ws && !aligned(workspace, 16)))
         return DP_ERR_INVALID_ARG;

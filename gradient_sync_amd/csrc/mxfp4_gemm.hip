@@ -83,21 +83,31 @@ __device__ __forceinline__ u32x4 quantize_block(const MxGemmParams &p, long long
             for (int i = 0; i < 4; ++i) x[h * 4 / W][h * 4 % W + i] = v[i];
         }
     } else {
-        // the row's last, short block, in small loops: rare, and it must not cost the others registers
+        // the row's last, short block, 8 values at a time and twice over, so
+        // that this rare case costs the others no registers; 8 loads are issued
+        // together, from the row's last value where there is none
         const int n = (int)(p.k - c0);
-        auto value = [&](int i) __attribute__((always_inline)) {     // i < n
-            return XT == kBF16 ? (unsigned)reinterpret_cast<const unsigned short *>(at)[i] << 16
-                               : reinterpret_cast<const unsigned *>(at)[i];
+        auto values = [&](int o, unsigned (&y)[8]) __attribute__((always_inline)) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const int j = min(8 * o + i, n - 1);
+                const unsigned v = XT == kBF16 ? (unsigned)reinterpret_cast<const unsigned short *>(at)[j] << 16
+                                               : reinterpret_cast<const unsigned *>(at)[j];
+                y[i] = 8 * o + i < n ? v : 0u;
+            }
         };
+        unsigned y[8];
 #pragma unroll 1
-        for (int i = 0; i < n; ++i) top = mx_max_f32(top, value(i));
+        for (int o = 0; 8 * o < n; ++o) {
+            values(o, y);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) top = mx_max_f32(top, y[i]);
+        }
         byte = mx_scale_byte(top);
         u32x4 code = {};
 #pragma unroll 1
-        for (int o = 0; o < 4 && byte != 255u; ++o) {
-            unsigned y[8];
-#pragma unroll
-            for (int i = 0; i < 8; ++i) y[i] = 8 * o + i < n ? value(8 * o + i) : 0u;
+        for (int o = 0; 8 * o < n && byte != 255u; ++o) {
+            values(o, y);
             const unsigned w = mx_pack8(y, mx_scale(byte));
 #pragma unroll
             for (int i = 0; i < 4; ++i) code[i] = i == o ? w : code[i];
@@ -613,6 +623,20 @@ hipError_t launch_typed(const MxGemmParams &p, int x_dt, hipStream_t stream)
 }
 
 }  // namespace
+
+// Every workgroup of 16 columns quantises the rows it needs, at 6e-5 us a row and
+// column of x while up to 384 of them run side by side; a launch that does it
+// once costs 4 us. Measured, one launch against two: 14336 x 4096, 4 rows 8.4
+// and 10.3 us, 12 rows 12.3 and 11.5; 4096 x 14336, 4 rows 10.0 and 10.9, 6 rows 11.9
+// and 11.0; 4096 x 4096, 16 rows 6.8 and 8.2. A row that ends inside a block costs
+// 1 us more, as that block is read piece by piece: 1000 x 500, 2 rows 4.1 and
+// 7.4, 8 rows 10.3 and 7.1.
+bool mx_quantize_inside(long long m, long long n, long long k)
+{
+    if (m > kMxFewRows) return false;
+    const double groups = (double)((n + 15) / 16);
+    return (double)m * ((double)k * 6e-5 * std::max(1.0, groups / 384) + (k % 32 ? 1.0 : 0.0)) <= 4.0;
+}
 
 hipError_t launch_mxfp4_gemm(const MxGemmParams &p, int c_dt, int x_dt, hipStream_t stream)
 {

@@ -48,7 +48,9 @@ struct MxGemmParams {
     long long m, n, k;
     int accumulate;                 // add to c (fp32)
 };
-constexpr int kMxFewRows = 16;      // rows up to which x is taken as it is
+constexpr int kMxFewRows = 16;      // rows up to which x may be taken as it is
+// whether a product of m rows of plain values quantises them inside
+bool mx_quantize_inside(long long m, long long n, long long k);
 // x_dt < 0: a is given as codes
 hipError_t launch_mxfp4_gemm(const MxGemmParams &p, int c_dt, int x_dt, hipStream_t stream);
 

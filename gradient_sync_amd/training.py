@@ -305,7 +305,7 @@ def dp_mxfp4_linear(x, w: Mxfp4, out=None, dtype=torch.bfloat16, stream=None):
     if k != w.cols:
         raise ValueError("dp_mxfp4_linear: x and w differ in length")
     out = _output(out, (m, w.rows), dtype, x, stream, "out")
-    need = lib().dp_mxfp4_linear_ws_bytes(m, k)
+    need = lib().dp_mxfp4_linear_ws_bytes(m, w.rows, k)
     ws = _empty(x, (need,), torch.uint8, stream) if need else None
     _check(lib().dp_mxfp4_linear(x.data_ptr(), ldx, _DTYPES[x.dtype], w.codes.data_ptr(),
                                  w.scales.data_ptr(), out.data_ptr(), m, w.rows, k,

@@ -581,11 +581,12 @@ dp_status_t dp_gemm_mxfp4(const void *a, const void *a_scales, const void *b, co
 /*
  * y[m,n] = Q(x)[m,kk] . w[n,kk]^T with x plain (DP_F32 or DP_BF16, row stride
  * ldx) and w quantised: dp_mxfp4_quantize and dp_gemm_mxfp4 in one call, the
- * same bits. Up to 16 rows (single tokens) x is quantised inside the product, in
- * one launch and without a workspace; beyond, the workspace holds Q(x):
- * dp_mxfp4_linear_ws_bytes(m, kk) bytes, 16-byte aligned.
+ * same bits. A few rows (a single token; up to 16, fewer for large n and kk) are
+ * quantised inside the product, in one launch and without a workspace;
+ * otherwise the workspace holds Q(x): dp_mxfp4_linear_ws_bytes(m, n, kk) bytes,
+ * 16-byte aligned (0: none needed, workspace may be NULL).
  */
-size_t dp_mxfp4_linear_ws_bytes(int64_t m, int64_t kk);
+size_t dp_mxfp4_linear_ws_bytes(int64_t m, int64_t n, int64_t kk);
 dp_status_t dp_mxfp4_linear(const void *x, int64_t ldx, int x_dt, const void *w,
                             const void *w_scales, void *y, int64_t m, int64_t n, int64_t kk,
                             int y_dt, void *workspace, void *stream);

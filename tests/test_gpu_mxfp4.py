@@ -257,7 +257,7 @@ def test_product_of_extreme_scales_and_nan_blocks():
 @pytest.mark.parametrize("x_dtype", [F32, BF16])
 @pytest.mark.parametrize("m", [1, 2, 15, 16, 17, 64, 130])
 def test_linear_is_quantize_and_product(m, x_dtype):
-    for n, k in ((100, 100), (48, 1024), (33, 2085)):
+    for n, k in ((100, 100), (48, 1024), (33, 2085), (40, 500), (6500, 6000)):
         x = rand((m, k + 3), 5, x_dtype)[:, 1:1 + k] if m > 1 else rand((m, k), 5, x_dtype)
         if k > 1000:
             x[0, 40] = float("nan")

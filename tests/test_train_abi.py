@@ -111,8 +111,11 @@ def test_sizes():
     assert L.dp_mxfp4_code_bytes(3, 129) == 3 * 128 and L.dp_mxfp4_code_bytes(0, 5) == 0
     assert L.dp_mxfp4_scale_bytes(17, 513) == 2 * 2 * 256
     assert L.dp_mxfp4_code_bytes(-1, 5) == 0 and L.dp_mxfp4_scale_bytes(1, 1 << 25) == 0
-    assert L.dp_mxfp4_linear_ws_bytes(16, 4096) == 0
-    assert L.dp_mxfp4_linear_ws_bytes(17, 100) == 17 * 64 + 192 + 512
+    assert L.dp_mxfp4_linear_ws_bytes(16, 1000, 4096) == 0
+    assert L.dp_mxfp4_linear_ws_bytes(1, 1 << 14, 14336) == 0
+    assert L.dp_mxfp4_linear_ws_bytes(16, 1 << 15, 14336) == 16 * 7168 + 28 * 256
+    assert L.dp_mxfp4_linear_ws_bytes(17, 1000, 100) == 17 * 64 + 192 + 512
+    assert L.dp_mxfp4_linear_ws_bytes(-1, 10, 100) == 0
 
 
 def test_quantize_refusals():
