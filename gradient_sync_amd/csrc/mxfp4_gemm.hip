@@ -327,7 +327,7 @@ __device__ __forceinline__ void mx_settle() { asm volatile("s_nop 15\n\ts_nop 15
 // selector does both. Rows past M or N are loads of the last row, and their
 // results are not stored.
 //
-// Measured: 8192^3 224-231 us (4.8-4.9 PFLOP/s; matrix units busy 57-65% of the
+// Measured: 8192^3 224-251 us on several cards (4.4-4.9 PFLOP/s; matrix units busy 57-65% of the
 // waves' cycles at a clock of 1.9 GHz that the card's power sets: zeros take 185
 // us, and a loop of nothing but these instructions reaches 7.4 PFLOP/s on random
 // codes, 6.6 in the 32x32x64 form), 4096^3 35 us, 2048 x 4096 x 4096 21 (tiles of 128).

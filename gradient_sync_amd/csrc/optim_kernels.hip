@@ -190,10 +190,10 @@ __global__ __launch_bounds__(kNT) void grad_norm_kernel(const NormParams p)
 // step, and to nearest it would stand still relative to its block. 32 lanes of
 // a wave hold one block, so the two maxima are register exchanges.
 //
-// Bound by HBM: 200M elements in 64 shards (fp32 p, bf16 g and copy) take 1011
-// us with fp32 states (5.54 TB/s) and 617 with 8-bit ones, stochastically rounded
+// Bound by HBM: 200M elements in 64 shards (fp32 p, bf16 g and copy) take 990
+// us with fp32 states (5.65 TB/s) and 618 with 8-bit ones, stochastically rounded
 // (5.22 TB/s); with bf16 p and stochastic rounding the vector units bound it
-// (460 us, 4.4 TB/s). One chunk per workgroup: workgroups that go through
+// (454 us, 4.5 TB/s). One chunk per workgroup: workgroups that go through
 // several load nothing while they compute and store (1245 us against 1005).
 constexpr int kAdamU = 2;                        // groups of 4 elements per thread and chunk
 constexpr int kAdamChunk = kNT * 4 * kAdamU;
