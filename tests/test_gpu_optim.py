@@ -275,6 +275,26 @@ def test_random_rounding_is_reproducible_and_unbiased():
     assert abs(corr(up[0][keep], up[0].roll(1)[keep])) < 0.01
 
 
+def test_random_rounding_goes_by_a_tensors_place_in_the_call():
+    """The second launch of a long list goes on counting: a tensor rounds as it does in a list of empty ones."""
+    k, n, one = 70, 700, 66
+    g = [rand(n, 0.1, i) for i in range(k)]
+
+    def run(keep):
+        gs = [x if keep(i) else x[:0] for i, x in enumerate(g)]
+        p = [torch.zeros_like(x) for x in gs]
+        m, v, s = dps.AdamW.new_state(p, 8)
+        dps.dp_adamw(p, gs, m, v, step=2, scales=s, lr=LR, seed=11)
+        return m[one], v[one]
+    whole, alone = run(lambda i: True), run(lambda i: i == one)
+    assert torch.equal(whole[0], alone[0]) and torch.equal(whole[1], alone[1])
+    other = [g[one]] * k
+    p = [torch.zeros_like(x) for x in other]
+    m, v, s = dps.AdamW.new_state(p, 8)
+    dps.dp_adamw(p, other, m, v, step=2, scales=s, lr=LR, seed=11)
+    assert torch.equal(m[one], whole[0]) and not torch.equal(m[one], m[one - 64]) and not torch.equal(m[1], m[2])
+
+
 def test_8_bit_training_follows_32_bit_training():
     """200 steps on a quadratic with beta2 = 0.999: random rounding keeps the second moment moving."""
     n = 4096
