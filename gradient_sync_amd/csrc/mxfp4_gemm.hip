@@ -252,7 +252,7 @@ hipError_t launch_few(const MxGemmParams &p, int x_dt, hipStream_t stream)
 
 // Workgroup id -> tile of C: ids go round-robin to the 8 XCDs, so each XCD is
 // handed a contiguous range of tiles, 4 tile rows at a time, and its L2 holds
-// the rows of A and B that its workgroups share.
+// the rows of A and B that its workgroups share (2, 8 or 16 rows: within 2%).
 __device__ __forceinline__ void tile_of(int id, int tiles_m, int tiles_n, int &tm, int &tn)
 {
     const int total = tiles_m * tiles_n;
@@ -507,7 +507,8 @@ __global__ __launch_bounds__(256) void mxfp4_gemm_tile_kernel(const MxGemmParams
         const long long row = m0 + wi * 16 * WB + i, col = n0 + wj * 16 * WB;
         if constexpr (VEC) {
             // pairs of blocks trade halves between lane rows g and g ^ 1, so that a
-            // lane holds 8 consecutive columns: one 16-byte store
+            // lane holds 8 consecutive columns: one 16-byte store (nontemporal: 1% slower at
+        // k 4096, 10% at k 1024)
             typedef unsigned short u16;
             const long long c8 = col + 16 * (g & 1) + 8 * (g >> 1);
             u16 *c = reinterpret_cast<u16 *>(p.c) + row * p.n + c8;
