@@ -1,0 +1,69 @@
+"""Gradient norm and AdamW where fp32 gets thin: subnormal second moments, states that are not numbers,
+and clip factors beyond fp32. u = 2^-24 is one fp32 rounding; each tolerance counts them."""
+import math
+
+import pytest
+import torch
+
+import gradient_sync_amd as dps
+from tests.helpers import say
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda"
+U = 2.0 ** -24
+F32, BF16 = torch.float32, torch.bfloat16
+
+
+def signs(n, seed):
+    return 1.0 - 2.0 * torch.randint(0, 2, (n,), generator=torch.Generator().manual_seed(seed))
+
+
+def uniform(n, lo, hi, seed):
+    return lo + (hi - lo) * torch.rand(n, generator=torch.Generator().manual_seed(seed), dtype=torch.float64)
+
+
+def held(x, scales, at):
+    """What 8-bit codes stand for."""
+    return x.view(torch.float8_e4m3fn).float().double() * scales.view(-1, 2)[:, at].double().repeat_interleave(128)[:x.numel()]
+
+
+# ------------------------------------------------------------------ subnormal second moments
+
+def test_root_of_a_subnormal_second_moment():
+    """eps = 0 and no gradient, so that the update is -2 lr m / (root(v) / root(1/2)) with m and v halved."""
+    n = 100_000
+    v0 = torch.exp2(uniform(n, -147, -120, 1)).float()
+    m0 = (v0.double().sqrt() * (0.5 + torch.rand(n, generator=torch.Generator().manual_seed(2))) * signs(n, 3)).float()
+    p, g, m, v = torch.zeros(n, device=DEV), torch.zeros(n, device=DEV), m0.to(DEV), v0.to(DEV)
+    say("root of a subnormal")
+    dps.dp_adamw([p], [g], [m], [v], step=1, lr=1.0, betas=(0.5, 0.5), eps=0.0, weight_decay=0.0)
+    v, p = v.cpu().double(), p.cpu().double()
+    assert torch.equal(m.cpu(), m0 * 0.5) and bool(((v - v0.double() / 2).abs() <= 2.0 ** -150).all()) and bool((v > 0).all())
+    want = -2.0 * (m0.double() / 2) / (v.sqrt() * math.sqrt(2.0))
+    # root 1, its factor 1 and product 1, quotient 3 (a reciprocal to 2 and a product), step size 0 and product 1
+    assert bool(((p - want).abs() <= 7.01 * U * want.abs()).all()), float(((p - want).abs() / want.abs()).max())
+
+
+@pytest.mark.parametrize("seed", [None, 5])
+def test_eight_bit_states_of_a_subnormal_second_moment(seed):
+    """The root of the smallest second moments is far above 2^-100: it is kept, and the step stays one of lr."""
+    n = 128 * 300
+    e = uniform(n // 128, -73, -61, 4).repeat_interleave(128) + uniform(n, 0, 1, 5)
+    g0 = (torch.exp2(e) * signs(n, 6)).float()
+    p, g = torch.zeros(n, device=DEV), g0.to(DEV)
+    m, v, s = dps.AdamW.new_state([p], 8)
+    say("8-bit subnormal", seed)
+    dps.dp_adamw([p], [g], m, v, scales=s, step=1, lr=1.0, betas=(0.5, 0.5), eps=0.0, weight_decay=0.0, seed=seed)
+    m2, v2 = g0.double() / 2, ((g0 * g0) * 0.5).double()
+    r2 = v2.sqrt()
+    assert bool((r2 > 0).all())
+    want = -2.0 * m2 / (r2 * math.sqrt(2.0))
+    assert bool(((p.cpu().double() - want).abs() <= 7.01 * U * want.abs()).all())
+    for at, x in ((0, m2), (1, r2)):
+        code, scale = (m, v)[at][0].cpu(), s[0].cpu().double().view(-1, 2)[:, at]
+        top = x.abs().view(-1, 128).amax(1)
+        assert bool(((scale * 448 - top).abs() <= 4 * U * top).all())
+        assert bool((code.view(-1) & 0x7F != 0).all())
+        steps = 1 if seed is None else 2
+        slack = steps * (2.0 ** -4 * x.abs() + 2.0 ** -10 * scale.repeat_interleave(128)) * (1 + 8 * U)
+        assert bool(((held(code, s[0].cpu(), at) - x).abs() <= slack).all())
