@@ -437,8 +437,10 @@ __device__ __forceinline__ void adam_chunk(const AdamParams &k, const AdamTensor
             r[u][i] = root(v[u][i]);
             // a hardware reciprocal (1 ulp) in place of a division: it enters the
             // parameter alone, at 2^-23 of the update. A denominator below
-            // the normal numbers, whose reciprocal could overflow, counts as 2^-126
-            const float den = fmaxf(r[u][i] * c.inv_sqrt_bc2 + k.eps, 0x1p-126f);
+            // the normal numbers, whose reciprocal could overflow, counts as 2^-126; a
+            // maximum would pass a NaN over, and take a step over 2^-126 in its place
+            float den = r[u][i] * c.inv_sqrt_bc2 + k.eps;
+            den = den < 0x1p-126f ? 0x1p-126f : den;
             p[u][i] = p[u][i] * k.decay - m[u][i] * __builtin_amdgcn_rcpf(den) * c.step_size;
             if constexpr (S8) {
                 top[u][0] = fmaxf(top[u][0], fabsf(m[u][i]));

@@ -473,7 +473,9 @@ dp_status_t dp_grad_norm(int nt, const int64_t *counts, const void *const *grads
  *   p = p (1 - lr weight_decay)
  *       - lr / (1 - beta1^t) * m / (sqrt(v) / sqrt(1 - beta2^t) + eps)
  * with t = opts->step, or ctrl->step where opts->step is 0. With ctrl->scale = 0
- * nothing is changed.
+ * nothing is changed. A denominator below 2^-126 (eps smaller than that, v zero)
+ * counts as 2^-126: an element without history or gradient stays where it is
+ * with eps = 0 too. A NaN in p, g, m or v gives a NaN in p.
  *   params[i] : p_dt, updated in place; DP_BF16 is rounded to nearest even
  *   grads[i]  : g_dt
  *   copies    : NULL, or for DP_F32 parameters bf16 copies of the new values
@@ -506,7 +508,8 @@ dp_status_t dp_adamw(int nt, const int64_t *counts, void *const *params, int p_d
  * never held as zero but at least as the smallest code. The parameters are
  * updated from the new m and v before these are rounded. All-zero
  * codes and scales are the initial state. Without ctrl a NaN gradient leaves its
- * element's states NaN, and an infinite one its block's.
+ * element's states NaN, and an infinite one its block's. So does a finite one
+ * whose square is beyond fp32, for v (a max_norm below 2^63 keeps g from that).
  *   Rounding: to nearest even; with DP_ADAMW_STOCHASTIC to one of the two
  *   neighbours, with probability in proportion, from 16 bits r of a
  *   counter-based generator: |y| -> floor(|y| / u + r / 65536) u, u the step

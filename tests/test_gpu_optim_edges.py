@@ -67,3 +67,22 @@ def test_eight_bit_states_of_a_subnormal_second_moment(seed):
         steps = 1 if seed is None else 2
         slack = steps * (2.0 ** -4 * x.abs() + 2.0 ** -10 * scale.repeat_interleave(128)) * (1 + 8 * U)
         assert bool(((held(code, s[0].cpu(), at) - x).abs() <= slack).all())
+
+
+# ------------------------------------------------------------------ states that are not numbers
+
+@pytest.mark.parametrize("bits", [32, 8])
+def test_a_second_moment_that_is_nan_shows_in_the_parameter(bits):
+    n, at = 1000, 300
+    p, g = [torch.full((n,), 2.0, device=DEV)], [torch.full((n,), 0.5, device=DEV)]
+    m, v, s = dps.AdamW.new_state(p, bits)
+    if bits == 32:
+        v[0][at] = float("nan")
+    else:
+        s[0].fill_(1.0)
+        v[0][at] = 0x7F
+    say("NaN second moment", bits)
+    dps.dp_adamw(p, g, m, v, scales=s, step=1, lr=0.125, weight_decay=0.0)
+    assert bool(torch.isfinite(p[0]).sum() == n - 1) and bool(p[0][at].isnan())
+    keep = torch.arange(n, device=DEV) != at
+    assert bool((p[0][keep] == p[0][0]).all()) and abs(float(p[0][0]) - 1.875) < 1e-5
