@@ -506,7 +506,8 @@ dp_status_t dp_adamw(int nt, const int64_t *counts, void *const *params, int p_d
  * new scales are the block's largest |m| and sqrt(v) over 448 (zero, with zero
  * codes, where that largest value is below 2^-100). A positive sqrt(v) is
  * never held as zero but at least as the smallest code. The parameters are
- * updated from the new m and v before these are rounded. All-zero
+ * updated from the new m and v before these are rounded, the quotient within 2
+ * places (2^-23) of the fp32 one. All-zero
  * codes and scales are the initial state. Without ctrl a NaN gradient leaves its
  * element's states NaN, and an infinite one its block's. So does a finite one
  * whose square is beyond fp32, for v (a max_norm below 2^63 keeps g from that).

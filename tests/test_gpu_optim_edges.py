@@ -2,6 +2,7 @@
 and clip factors beyond fp32. u = 2^-24 is one fp32 rounding; each tolerance counts them."""
 import math
 
+import numpy as np
 import pytest
 import torch
 
@@ -86,3 +87,31 @@ def test_a_second_moment_that_is_nan_shows_in_the_parameter(bits):
     assert bool(torch.isfinite(p[0]).sum() == n - 1) and bool(p[0][at].isnan())
     keep = torch.arange(n, device=DEV) != at
     assert bool((p[0][keep] == p[0][0]).all()) and abs(float(p[0][0]) - 1.875) < 1e-5
+
+
+# ------------------------------------------------------------------ bit for bit
+
+def test_adamw_with_fp32_states_is_the_formula_rounded_as_written():
+    """Every operation rounded to nearest once, in the order of the formula: second moments of every exponent,
+    subnormal ones among them, and of random fractions."""
+    n, t = 1 << 20, 4
+    lr, (b1, b2), eps, wd = 0.01, (0.9, 0.95), 1e-30, 0.1
+    gen = torch.Generator().manual_seed(7)
+    v0 = torch.randint(1, 0x7F000000, (n,), generator=gen, dtype=torch.int32).view(F32)
+    v0[:4096] = torch.arange(1, 4097, dtype=torch.int32).view(F32)
+    v0[4096:4200] = 0
+    m0 = (v0.double().sqrt() * torch.randn(n, generator=gen, dtype=torch.float64)).float()
+    g0 = (v0.double().sqrt() * torch.randn(n, generator=gen, dtype=torch.float64)).float()
+    p0 = torch.randn(n, generator=gen)
+    p, g, m, v = (x.to(DEV) for x in (p0, g0, m0, v0))
+    say("bit for bit")
+    dps.dp_adamw([p], [g], [m], [v], step=t, lr=lr, betas=(b1, b2), eps=eps, weight_decay=wd)
+    f = lambda x: np.float32(x)
+    p0, g0, m0, v0 = (x.numpy() for x in (p0, g0, m0, v0))
+    with np.errstate(all="ignore"):
+        m2 = m0 * f(b1) + g0 * f(1 - b1)
+        v2 = v0 * f(b2) + (g0 * g0) * f(1 - b2)
+        den = np.sqrt(v2) * f(1 / math.sqrt(1 - b2 ** t)) + f(eps)
+        want = p0 * f(1 - lr * wd) - m2 / den * f(lr / (1 - b1 ** t))
+    for got, x in ((m, m2), (v, v2), (p, want)):
+        assert x.dtype == np.float32 and np.array_equal(got.cpu().numpy(), x)
