@@ -191,7 +191,7 @@ dp_status_t dp_grad_norm(int nt, const int64_t *counts, const void *const *grads
     p.partial = (double *)workspace;
     p.ticket = (unsigned *)((char *)workspace + dps::kNormMaxGrid * sizeof(double));
     p.ctrl = (dps::StepCtrl *)ctrl;
-    p.max_norm = (float)max_norm;
+    p.max_norm = max_norm;
     int i = 0;
     do {
         p.nt = 0;

@@ -25,7 +25,7 @@ struct NormParams {
     int nt;
     int add;                        // add to the partials of an earlier launch
     int finish;                     // the call's last launch: the last workgroup sums up
-    float max_norm;
+    double max_norm;
     double *partial;
     unsigned *ticket;
     StepCtrl *ctrl;

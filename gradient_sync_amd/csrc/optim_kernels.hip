@@ -160,9 +160,11 @@ __global__ __launch_bounds__(kNT) void grad_norm_kernel(const NormParams p)
         const float nf = (float)norm;
         const bool fine = nf < __builtin_inff();      // false for NaN too
         p.ctrl->norm = nf;
+        // zero is what tells the update to skip: a factor too small for fp32 is its
+        // smallest number
         p.ctrl->scale = !fine ? 0.0f
-                        : p.max_norm > 0.0f && norm > (double)p.max_norm ? (float)((double)p.max_norm / norm)
-                                                                         : 1.0f;
+                        : p.max_norm > 0.0 && norm > p.max_norm ? fmaxf((float)(p.max_norm / norm), 0x1p-149f)
+                                                                : 1.0f;
         if (fine)
             p.ctrl->step += 1;
         else

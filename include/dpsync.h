@@ -452,8 +452,8 @@ typedef struct {
 /*
  * norm = sqrt(sum of the squares of all elements of all tensors), summed in
  * fp64 in a fixed order (the same bits in every run), and the clip factor:
- *   finite norm : scale = max_norm / norm if max_norm > 0 and norm > max_norm,
- *                 else 1; step += 1
+ *   finite norm : scale = max_norm / norm (at least 2^-149) if max_norm > 0 and
+ *                 norm > max_norm, else 1; step += 1
  *   otherwise   : scale = 0; skipped += 1
  * (a norm beyond fp32 counts as not finite).
  *   grads[i]  : counts[i] elements of dt (DP_F32 or DP_BF16)
@@ -507,7 +507,7 @@ dp_status_t dp_adamw(int nt, const int64_t *counts, void *const *params, int p_d
  * codes, where that largest value is below 2^-100). A positive sqrt(v) is
  * never held as zero but at least as the smallest code. The parameters are
  * updated from the new m and v before these are rounded, the quotient within 2
- * places (2^-23) of the fp32 one. All-zero
+ * places of the fp32 one. All-zero
  * codes and scales are the initial state. Without ctrl a NaN gradient leaves its
  * element's states NaN, and an infinite one its block's. So does a finite one
  * whose square is beyond fp32, for v (a max_norm below 2^63 keeps g from that).

@@ -115,3 +115,26 @@ def test_adamw_with_fp32_states_is_the_formula_rounded_as_written():
         want = p0 * f(1 - lr * wd) - m2 / den * f(lr / (1 - b1 ** t))
     for got, x in ((m, m2), (v, v2), (p, want)):
         assert x.dtype == np.float32 and np.array_equal(got.cpu().numpy(), x)
+
+
+# ------------------------------------------------------------------ clip factors beyond fp32
+
+@pytest.mark.parametrize("value,most", [(1e30, 1e-30), (1e37, 1e-9), (3.0, 1e-46), (1e20, 1e-300), (2.0, 1e-45)])
+def test_a_finite_norm_far_above_the_bound_still_steps(value, most):
+    """The factor is max_norm / norm rounded once, and where fp32 has nothing so small its smallest number:
+    zero means that the step is skipped, and this one counts."""
+    g = [torch.full((100,), value, device=DEV)]
+    say("clip", value, most)
+    ctrl = dps.dp_grad_norm(g, max_norm=most)
+    want = most / (float(torch.tensor(value, dtype=F32)) * 10)
+    assert int(ctrl.step) == 1 and int(ctrl.skipped) == 0
+    assert abs(float(ctrl.scale) - want) <= U * want + 2.0 ** -149 and float(ctrl.scale) > 0
+    p = [torch.full((100,), 4.0, device=DEV)]
+    m, v, _ = dps.AdamW.new_state(p)
+    dps.dp_adamw(p, g, m, v, ctrl=ctrl, lr=0.5, weight_decay=0.5)
+    assert bool((p[0] <= 3.01).all())                # at least the decay was made
+
+
+def test_a_bound_beyond_fp32_clips_nothing():
+    ctrl = dps.dp_grad_norm([torch.full((4,), 1e38, device=DEV)], max_norm=1e39)
+    assert float(ctrl.scale) == 1.0 and int(ctrl.step) == 1
