@@ -95,9 +95,16 @@ class StepCtrl:
 class GradNorm:
     """Global 2-norm of a list of gradients and the factor that clips it
     (dp_grad_norm). `run` advances ctrl.step, or ctrl.skipped where the norm is
-    not finite, and returns ctrl."""
+    not finite, and returns ctrl. It may run on any stream, one run at a time."""
 
     def __init__(self, grads, ctrl: StepCtrl | None = None):
+        self._build(grads, ctrl)
+        # a run on another stream than this one finds its workspace zeroed (a
+        # stream that captures cannot wait; what it captures is in order)
+        if not torch.cuda.is_current_stream_capturing():
+            torch.cuda.current_stream(self.workspace.device).synchronize()
+
+    def _build(self, grads, ctrl):
         self.grads = _list(grads, "grads", _FLOATS)
         device = self.grads[0].device if self.grads else "cuda"
         self.ctrl = StepCtrl(device=device) if ctrl is None else ctrl
@@ -185,8 +192,9 @@ class AdamW:
 
 def dp_grad_norm(grads, ctrl: StepCtrl | None = None, max_norm: float = 0.0, stream=None) -> StepCtrl:
     """GradNorm(grads, ctrl).run(max_norm), for a list that is used once."""
-    with _on(stream):
-        norm = GradNorm(grads, ctrl)
+    norm = GradNorm.__new__(GradNorm)
+    with _on(stream):                # the stream of its only run: nothing to wait for
+        norm._build(grads, ctrl)
     return norm.run(max_norm, stream)
 
 

@@ -138,3 +138,24 @@ def test_a_finite_norm_far_above_the_bound_still_steps(value, most):
 def test_a_bound_beyond_fp32_clips_nothing():
     ctrl = dps.dp_grad_norm([torch.full((4,), 1e38, device=DEV)], max_norm=1e39)
     assert float(ctrl.scale) == 1.0 and int(ctrl.step) == 1
+
+
+# ------------------------------------------------------------------ streams
+
+def test_a_norm_built_behind_other_work_runs_on_another_stream():
+    """The workspace's fill is queued behind work on the stream where the norm is built, and the run does not
+    wait for that stream."""
+    g = [torch.full((1000 + i,), 0.5, device=DEV) for i in range(200)]
+    want = math.sqrt(sum(x.numel() for x in g)) * 0.5
+    side, ctrl = torch.cuda.Stream(), dps.StepCtrl()
+    busy = torch.ones(1 << 28, device=DEV)
+    torch.cuda.synchronize()
+    for i in range(3):
+        for _ in range(20):
+            busy.mul_(1.0)
+        norm = dps.GradNorm(g, ctrl)
+        say("norm on another stream", i)
+        norm.run(1.0, stream=side)
+        side.synchronize()
+        assert int(ctrl.step) == i + 1 and abs(float(ctrl.norm) - want) <= 1.01 * U * want
+        torch.cuda.synchronize()
