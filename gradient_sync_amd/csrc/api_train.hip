@@ -19,7 +19,9 @@ static_assert(DP_STATE_BLOCK == dps::kStateBlock, "state block sizes differ");
 namespace {
 
 constexpr int64_t kMaxDim = (int64_t)1 << 24;
-constexpr int64_t kMaxOut = (int64_t)1 << 40;   // elements of a product: its grid fits 31 bits
+// Elements of a product: its tiles of 128 x 128 are then fewer than a launch's
+// workgroups, edges included (2^23 + 2^18 of 2^24 - 1).
+constexpr int64_t kMaxOut = (int64_t)1 << 37;
 
 struct Range {
     uintptr_t lo, hi;
@@ -249,8 +251,8 @@ dp_status_t dp_mxfp4_quantize(const void *src, int64_t rows, int64_t cols, int64
     const int es = dps::elem_size(dt);
     if (!aligned(src, (uintptr_t)es) || (codes && !mx_operand_ok(codes, scales)) ||
         (codes_t && !mx_operand_ok(codes_t, scales_t)) ||
-        ((rows + 127) / 128) * ((cols + 127) / 128) > 0x3fffffffLL ||
-        (rows + 15) / 16 * dps::mx_scale_tiles(cols) > 0x7fffffffLL)
+        (codes_t && (rows + 127) / 128 * ((cols + 127) / 128) > dps::kMaxGroups256) ||
+        (!codes_t && (rows + 15) / 16 * dps::mx_scale_tiles(cols) > dps::kMaxGroups256))
         return DP_ERR_INVALID_ARG;
     Range r[5];
     size_t n = 0;

@@ -9,6 +9,22 @@ namespace dps {
 // where it failed.
 int hip_failure_code(hipError_t e);
 
+// A launch has fewer than 2^32 work-items: that many workgroups of 256 threads.
+constexpr long long kMaxGroups256 = 0xffffffffLL / 256;
+// launch(first, grid) for the workgroups first .. first + grid - 1 of `groups`, in as
+// many launches as they take
+template <typename F>
+hipError_t launch_groups256(long long groups, F launch)
+{
+    hipError_t e = hipSuccess;
+    for (long long first = 0; first < groups && e == hipSuccess; first += kMaxGroups256) {
+        const long long rest = groups - first;
+        launch((unsigned)first, (unsigned)(rest < kMaxGroups256 ? rest : kMaxGroups256));
+        e = hipGetLastError();
+    }
+    return e;
+}
+
 // Batched fp32 GEMM on MFMA: for each batch b < nb,
 // C_b[M,N] = op(A_b)[M,Kd] * op(B_b)[Kd,N], row-major; op(A) = A ([M,Kd]) or,
 // with trans_a, A^T where A_b is stored [Kd,M]; op(B) = B ([Kd,N]) or, with

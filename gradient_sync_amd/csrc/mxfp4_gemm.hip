@@ -138,7 +138,7 @@ __device__ __forceinline__ u32x4 quantize_block(const MxGemmParams &p, long long
 // single token (1 x 14336 x 4096: 15.5 us against 7.6, 31 MB read).
 constexpr int kPieces = 2;
 template <int MB, int CT, int XT>
-__global__ __launch_bounds__(256) void mxfp4_gemm_few_kernel(const MxGemmParams p)
+__global__ __launch_bounds__(256) void mxfp4_gemm_few_kernel(const MxGemmParams p, unsigned first)
 {
     __shared__ f32x4 part[3][MB][64];
     __shared__ __attribute__((aligned(16))) unsigned char xc[XT < 0 ? 1 : 4 * kPieces * 16 * 256];
@@ -148,8 +148,8 @@ __global__ __launch_bounds__(256) void mxfp4_gemm_few_kernel(const MxGemmParams 
     // instructions run whatever the lane mask says
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int i = lane & 15, g = lane >> 4;
-    const unsigned blocks_n = (unsigned)((p.n + 15) >> 4), bm = blockIdx.x / blocks_n;
-    const long long n0 = (long long)(blockIdx.x - bm * blocks_n) * 16, m0 = (long long)bm * 16 * MB;
+    const unsigned id = first + blockIdx.x, blocks_n = (unsigned)((p.n + 15) >> 4), bm = id / blocks_n;
+    const long long n0 = (long long)(id - bm * blocks_n) * 16, m0 = (long long)bm * 16 * MB;
     const long long pitch = mx_pitch(p.k), tiles = mx_scale_tiles(p.k);
     const int steps = (int)((p.k + 127) / 128);
     const long long rb = min(n0 + i, p.n - 1);
@@ -171,8 +171,8 @@ __global__ __launch_bounds__(256) void mxfp4_gemm_few_kernel(const MxGemmParams 
         unsigned char *codes = xc + wave * (kPieces * 4096), *bytes = xs + wave * (kPieces * 256);
         if constexpr (XT >= 0) {
             const int blocks = (int)p.m * 16 * kPieces;
-            for (int id = lane; id < blocks; id += 64) {
-                const int row = id / (16 * kPieces), h = id / 16 % kPieces, bk = id % 16;
+            for (int at = lane; at < blocks; at += 64) {
+                const int row = at / (16 * kPieces), h = at / 16 % kPieces, bk = at % 16;
                 const long long kb = (kt0 + h) * 16LL + bk;
                 unsigned byte = 0;
                 u32x4 code = {};
@@ -233,19 +233,14 @@ __global__ __launch_bounds__(256) void mxfp4_gemm_few_kernel(const MxGemmParams 
 template <int MB, int CT>
 hipError_t launch_few(const MxGemmParams &p, int x_dt, hipStream_t stream)
 {
-    const unsigned grid = (unsigned)((p.n + 15) / 16 * ((p.m + 16 * MB - 1) / (16 * MB)));
-    if constexpr (MB == 1) {
-        if (x_dt == kBF16) {
-            mxfp4_gemm_few_kernel<1, CT, kBF16><<<grid, 256, 0, stream>>>(p);
-            return hipGetLastError();
+    const long long groups = (p.n + 15) / 16 * ((p.m + 16 * MB - 1) / (16 * MB));
+    return launch_groups256(groups, [&](unsigned first, unsigned grid) {
+        if constexpr (MB == 1) {
+            if (x_dt == kBF16) return mxfp4_gemm_few_kernel<1, CT, kBF16><<<grid, 256, 0, stream>>>(p, first);
+            if (x_dt == kF32) return mxfp4_gemm_few_kernel<1, CT, kF32><<<grid, 256, 0, stream>>>(p, first);
         }
-        if (x_dt == kF32) {
-            mxfp4_gemm_few_kernel<1, CT, kF32><<<grid, 256, 0, stream>>>(p);
-            return hipGetLastError();
-        }
-    }
-    mxfp4_gemm_few_kernel<MB, CT, -1><<<grid, 256, 0, stream>>>(p);
-    return hipGetLastError();
+        mxfp4_gemm_few_kernel<MB, CT, -1><<<grid, 256, 0, stream>>>(p, first);
+    });
 }
 
 // ------------------------------------------------------------ tiled kernel

@@ -523,9 +523,9 @@ __device__ __forceinline__ void adam_chunk(const AdamParams &k, const AdamTensor
 }
 
 template <int PT, int GT, bool S8, bool SR>
-__global__ __launch_bounds__(kNT) void adamw_kernel(const AdamParams k)
+__global__ __launch_bounds__(kNT) void adamw_kernel(const AdamParams k, unsigned first)
 {
-    const int b = blockIdx.x;
+    const int b = (int)(first + blockIdx.x);
     // the last tensor that starts at or before this chunk, by halves (one tensor a
     // lane, a vector load and a ballot: 4% slower at 200M elements)
     int t = 0;
@@ -542,18 +542,18 @@ __global__ __launch_bounds__(kNT) void adamw_kernel(const AdamParams k)
 template <int PT, int GT>
 hipError_t launch_adamw_typed(const AdamParams &p, bool eight, bool stochastic, hipStream_t stream)
 {
-    const int grid = p.first[p.nt];
     // fp32 states: LDS that the kernel does not use keeps a CU at two workgroups,
     // 14 KiB a wave on their way, and their streams apart (200M elements: 977 us
     // for 1051 with eight; three to five 1006-1018). With 8-bit states a wave
     // computes longer and every one helps (578 us for 722).
-    if (!eight)
-        adamw_kernel<PT, GT, false, false><<<grid, kNT, 80 << 10, stream>>>(p);
-    else if (!stochastic)
-        adamw_kernel<PT, GT, true, false><<<grid, kNT, 0, stream>>>(p);
-    else
-        adamw_kernel<PT, GT, true, true><<<grid, kNT, 0, stream>>>(p);
-    return hipGetLastError();
+    return launch_groups256(p.first[p.nt], [&](unsigned first, unsigned grid) {
+        if (!eight)
+            adamw_kernel<PT, GT, false, false><<<grid, kNT, 80 << 10, stream>>>(p, first);
+        else if (!stochastic)
+            adamw_kernel<PT, GT, true, false><<<grid, kNT, 0, stream>>>(p, first);
+        else
+            adamw_kernel<PT, GT, true, true><<<grid, kNT, 0, stream>>>(p, first);
+    });
 }
 
 }  // namespace

@@ -547,6 +547,10 @@ dp_status_t dp_adamw8(int nt, const int64_t *counts, void *const *params, int p_
  *            of rows or blocks that do not exist are unspecified.
  * Row shards of a multiple of 16 rows are contiguous in both, so dp_all_gather
  * collects a quantised weight (as DP_I32: both sizes are multiples of 4).
+ * Rows and columns are at most 2^24 each. A matrix is quantised in at most
+ * 2^24 - 1 pieces, of 16 x 512 elements along its rows alone, else of 128 x 128,
+ * and expanded in fewer than 2^38 pieces of 8 elements of a row: more than one
+ * GPU's memory holds (else DP_ERR_INVALID_ARG).
  */
 size_t dp_mxfp4_code_bytes(int64_t rows, int64_t cols);
 size_t dp_mxfp4_scale_bytes(int64_t rows, int64_t cols);
@@ -572,7 +576,7 @@ dp_status_t dp_mxfp4_dequantize(const void *codes, const void *scales, int64_t r
  * c[m,n] = a[m,kk] . b[n,kk]^T of quantised operands, summed in fp32; c is
  * row-major and contiguous, DP_F32 or DP_BF16 (rounded once, to nearest even).
  * With accumulate (DP_F32 only) the product is added to c. m or n = 0 is a
- * no-op; kk >= 1; m n <= 2^40. c must not overlap an operand (DP_ERR_ALIAS).
+ * no-op; kk >= 1; m n <= 2^37. c must not overlap an operand (DP_ERR_ALIAS).
  * Training a linear layer y = x w^T on quantised operands:
  *   y[m,n]  = Q(x) . Q(w)^T                quantised along k
  *   dx[m,k] = Q(dy) . Q(w^T)^T             along n
