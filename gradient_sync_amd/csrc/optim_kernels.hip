@@ -543,12 +543,16 @@ template <int PT, int GT>
 hipError_t launch_adamw_typed(const AdamParams &p, bool eight, bool stochastic, hipStream_t stream)
 {
     // fp32 states: LDS that the kernel does not use keeps a CU at two workgroups,
-    // 14 KiB a wave on their way, and their streams apart (200M elements: 977 us
-    // for 1051 with eight; three to five 1006-1018). With 8-bit states a wave
-    // computes longer and every one helps (578 us for 722).
+    // 7 KiB a wave on their way, and their streams apart (fp32 parameters, 200M elements:
+    // 925 us for 985 with eight; 80M 360 for 379; 7M 34.8 for 35.2), but
+    // not where eight a CU take every chunk at once (2M: 9.5 us for 10.9; 4M 19.3 for
+    // 19.8; 1M, at most two a CU anyway, 6.7 and 6.7). With 8-bit states a wave computes
+    // longer and every one helps (200M elements: 578 us for 722).
+    constexpr int kCUs = 256, kPerCU = 8;
+    const unsigned lds = !eight && p.first[p.nt] > kPerCU * kCUs ? 80u << 10 : 0u;
     return launch_groups256(p.first[p.nt], [&](unsigned first, unsigned grid) {
         if (!eight)
-            adamw_kernel<PT, GT, false, false><<<grid, kNT, 80 << 10, stream>>>(p, first);
+            adamw_kernel<PT, GT, false, false><<<grid, kNT, lds, stream>>>(p, first);
         else if (!stochastic)
             adamw_kernel<PT, GT, true, false><<<grid, kNT, 0, stream>>>(p, first);
         else

@@ -17,7 +17,7 @@ static long long groups = 0, tensors_index = 0;
 static dim3 grid_, block_;
 static size_t shared_;
 static hipStream_t stream_;
-static bool parts = false, adam = false;
+static bool parts = false, adam = false, eight_bits = false;
 
 #define EXPECT(c)                                              \
     do {                                                       \
@@ -39,7 +39,7 @@ hipError_t __hipPopCallConfiguration(dim3 *grid, dim3 *block, size_t *shared, hi
     *grid = grid_, *block = block_, *shared = shared_, *stream = stream_;
     return hipSuccess;
 }
-hipError_t hipLaunchKernel(const void *, dim3 grid, dim3 block, void **args, size_t, hipStream_t)
+hipError_t hipLaunchKernel(const void *, dim3 grid, dim3 block, void **args, size_t shared, hipStream_t)
 {
     EXPECT(grid.x >= 1 && (unsigned long long)grid.x * block.x < 1ull << 32);
     EXPECT(grid.y == 1 && grid.z == 1 && block.y == 1 && block.z == 1);
@@ -50,6 +50,8 @@ hipError_t hipLaunchKernel(const void *, dim3 grid, dim3 block, void **args, siz
         if (p->index0 != tensors_index) groups = 0;
         tensors_index = p->index0;
         EXPECT(first == groups && first + (long long)grid.x <= p->first[p->nt]);
+        // fp32 states: two workgroups a CU, except where eight take all the chunks at once
+        EXPECT(shared == (!eight_bits && p->first[p->nt] > 2048 ? 80u << 10 : 0u));
     } else if (parts) {
         // the last argument is the first workgroup's number
         EXPECT(*(const unsigned *)args[1] == groups || *(const unsigned *)args[2] == groups);
@@ -81,11 +83,12 @@ int main(int, char **argv)
 
     // AdamW: 2^35 elements and more are 2^24 chunks of 2048
     adam = true;
-    for (int64_t n : {one, one << 20, (one << 35) - 2048, one << 35, (one << 35) + 5, one << 37}) {
+    for (int64_t n : {one, one << 20, 2048 * 2048 * one, 2048 * 2048 * one + 1, (one << 35) - 2048, one << 35, (one << 35) + 5, one << 37}) {
         void *p = a, *g = b, *m = c, *v = d, *s = e;
         dp_adamw_opts_t o = {1e-3, 0.9, 0.999, 1e-8, 0.01, 3, 7, 0, 0};
         for (bool eight : {false, true}) {
             fresh();
+            eight_bits = eight;
             if (eight) {
                 o.flags = DP_ADAMW_STOCHASTIC;
                 EXPECT(CALL(dp_adamw8)(1, &n, &p, DP_BF16, &g, DP_BF16, (uint8_t **)&m, (uint8_t **)&v, (float **)&s, nullptr, &o, nullptr, nullptr) == DP_OK);
@@ -103,6 +106,7 @@ int main(int, char **argv)
         for (int i = 0; i < 100; ++i) p[i] = c + (one << 34) * i, m[i] = d + (one << 34) * i, v[i] = e + (one << 34) * i;
         dp_adamw_opts_t o = {1e-3, 0.9, 0.999, 1e-8, 0.01, 3, 7, 0, 0};
         fresh();
+        eight_bits = false;
         EXPECT(CALL(dp_adamw)(100, n.data(), p.data(), DP_F32, g.data(), DP_F32, (float **)m.data(), (float **)v.data(), nullptr, &o, nullptr, nullptr) == DP_OK);
         EXPECT(launches == 5 && tensors_index == 64 && groups == 36ll << 19);   // 2^25 chunks in three, 36 x 2^19 in two
     }
