@@ -100,3 +100,32 @@ def test_few_row_products_branch_by_scalars(kernels):
                 if re.match(r"\.LBB", back) or "v_mfma" in back or "s_cbranch" in back:
                     break
                 assert "saveexec" not in back, name
+
+
+def test_tiles_in_turn_loop(kernels):
+    """The kernels that go through several tiles, pass by pass: between the matrix instructions of their loop over
+    K stands nothing but the choice of scale bytes; the choice of the next tile is one block apart, which a
+    pass that is not a tile's last jumps over; scalars kept in vector lanes are fetched outside the loop."""
+    several = {n: v for n, v in pick(kernels, "mxfp4_gemm_tile_kernelILi8").items() if "ELb1EEE" in n}
+    assert len(several) == 3
+    for name, (_, body) in several.items():
+        blocks = re.split(r"^(?=\.LBB\S+:|; %bb\.)", body, flags=re.M)
+        loop = [b for b in blocks if "Depth=2" in "\n".join(b.splitlines()[:3])]
+        assert sum(b.count("v_mfma") for b in loop) == body.count("v_mfma") == 256, name
+        vector = lambda b: set(re.findall(r"^\s*(v_\w+)", b, re.M)) - {"v_mfma_scale_f32_16x16x128_f8f6f4"}
+        change = []
+        for b in loop:
+            if "v_mfma" in b:
+                assert vector(b) <= {"v_perm_b32"}, (name, vector(b))
+            elif vector(b):
+                change.append(b)
+        assert len(change) == 1 and vector(change[0]) == {"v_mov_b32_e32"}, (name, [vector(b) for b in change])
+        assert len(re.findall(r"\bv_mov_b32", change[0])) <= 32, name
+        before = loop[loop.index(change[0]) - 1]
+        assert re.search(r"\bs_cbranch", before) and "v_mfma" not in before, name
+        # where the tile before left stores on their way, they are counted on top: in the two waits of an even stage
+        waits = sorted(int(n) for b in loop for n in re.findall(r"s_waitcnt vmcnt\((\d+)\)", b))
+        if "ILi8ELi1ELb1" in name:
+            assert len(waits) == 6 and waits[4] - 32 in waits[:4] and waits[5] - 32 in waits[:4], (name, waits)
+        else:
+            assert len(waits) == 4, (name, waits)
