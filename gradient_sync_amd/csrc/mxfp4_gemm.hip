@@ -322,10 +322,13 @@ __device__ __forceinline__ void mx_settle() { asm volatile("s_nop 15\n\ts_nop 15
 // selector does both. Rows past M or N are loads of the last row, and their
 // results are not stored.
 //
-// Measured: 8192^3 224-251 us on several cards (4.4-4.9 PFLOP/s; matrix units busy 57-65% of the
-// waves' cycles at a clock of 1.9 GHz that the card's power sets: zeros take 185
-// us, and a loop of nothing but these instructions reaches 7.4 PFLOP/s on random
-// codes, 6.6 in the 32x32x64 form), 4096^3 35 us, 2048 x 4096 x 4096 21 (tiles of 128).
+// Measured: 8192^3 224-251 us on several cards (4.4-4.9 PFLOP/s), 4096^3 35-37 us, 2048
+// x 4096 x 4096 22-24 (tiles of 128). Two things bound the large ones. The matrix units are
+// busy 57% (8192 x 14336 x 4096) to 67% (8192^3) of the cycles: waves wait 14% of them for
+// loads and each other and are held at issue in 30%, the LDS reads and loads going out between
+// the matrix instructions. And the card's power sets the clock, 1.66-1.77 GHz here:
+// codes of zero take 190 us, and a loop of nothing but these instructions runs at 1.68
+// GHz on random codes (6.8 PFLOP/s; 6.1 in the 32x32x64 form), at 2.38 on zeros (9.7).
 //
 // LOOP: a workgroup of the large tile has a CU to itself, so that nothing runs
 // while it starts and while it writes C. With more tiles than CUs, 256 workgroups

@@ -97,7 +97,7 @@ __global__ __launch_bounds__(kNT) void mxfp4_quantize_rows_kernel(const MxQuantP
 // 128 x 128, quantises its rows from registers, and its columns from LDS, a
 // thread 32 rows of two neighbouring columns. HBM-bound, with 9% more written
 // than needed (scale bytes leave one by one): 14336 x 4096 bf16 both ways in
-// 37.8 us (4.75 TB/s).
+// 37.8 us (4.75 TB/s), along the columns alone in 29.1 (5.1 TB/s).
 template <int DT, bool ROW>
 __global__ __launch_bounds__(kNT) void mxfp4_quantize_cols_kernel(const MxQuantParams p, int tiles_c)
 {

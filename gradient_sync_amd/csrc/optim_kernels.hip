@@ -30,8 +30,11 @@ typedef unsigned int u32_e __attribute__((aligned(1)));
 constexpr int kNT = 256;
 
 // Everything here is read once and written once per step: nontemporal, whatever
-// the alignment (AdamW of 200M elements
-// with fp32 states: 1245 us in place of 1389; the norm of 200M fp32: 117 for 131).
+// the alignment (the norm of 200M fp32 values: 117 us in place of 131; AdamW with
+// fp32 states and a copy, 200M elements 953 for 1035, 40M 187 for 209, up to 4M the
+// same. Steps of 7M to 20M elements one after the other, whose tensors then stay in
+// the 256 MB Infinity Cache, are 5 to 11% slower for it, 14M 66 us for 59: between the
+// steps of a training run its other work passes through that cache).
 #define DPS_ONCE(V)                                                                          \
     __device__ __forceinline__ V load_once(const V *p) { return __builtin_nontemporal_load(p); } \
     __device__ __forceinline__ void store_once(V *p, V v) { __builtin_nontemporal_store(v, p); }
@@ -53,8 +56,9 @@ __device__ __forceinline__ float bf16_at(const char *p, long long i)
 // overflows, and 10^9 terms lose nothing. Each thread holds four sums; a
 // workgroup's sum is a fixed tree over its threads, and the last workgroup to
 // finish adds the partials in a fixed order: the same bits in every run.
-// Bound by reading the gradients: 200M bf16 values in 62 us (6.45 TB/s), 10M
-// fp32 values in 12.5 (3.2 TB/s, the launch and the finish being half of it).
+// Bound by reading the gradients: 200M bf16 values in 62 us (6.45 TB/s), 200M fp32
+// ones in 117 (6.8 TB/s), 10M fp32 ones in 12.3 (3.3 TB/s: the launch, the finish, and
+// 1,224 chunks over 512 workgroups, three for some and two for others).
 constexpr int kNormChunk = 8192;
 
 template <int DT>
@@ -193,11 +197,12 @@ __global__ __launch_bounds__(kNT) void grad_norm_kernel(const NormParams p)
 // step, and to nearest it would stand still relative to its block. 32 lanes of
 // a wave hold one block, so the two maxima are register exchanges.
 //
-// Bound by HBM: 200M elements in 64 shards (fp32 p, bf16 g and copy) take 990
-// us with fp32 states (5.65 TB/s) and 618 with 8-bit ones, stochastically rounded
-// (5.22 TB/s); with bf16 p and stochastic rounding the vector units bound it
-// (454 us, 4.5 TB/s). One chunk per workgroup: workgroups that go through
-// several load nothing while they compute and store (1245 us against 1005).
+// Bound by HBM: 200M elements in 64 shards (fp32 p, bf16 g and copy) take 981
+// us with fp32 states (5.7 TB/s; 976-1037 in one run) and 585-634 with 8-bit ones,
+// stochastically rounded (5.1-5.5 TB/s); with bf16 p and g and stochastic rounding the
+// vector units bound it, at the clock that power leaves (474-555 us, 3.6-4.3 TB/s;
+// to nearest 385). One chunk per workgroup: workgroups that go through several load
+// nothing while they compute and store (1245 us against 1005, fp32 states).
 constexpr int kAdamU = 2;                        // groups of 4 elements per thread and chunk
 constexpr int kAdamChunk = kNT * 4 * kAdamU;
 

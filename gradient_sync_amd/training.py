@@ -4,8 +4,11 @@ Between the ReduceScatter that leaves each rank its gradient shards and the
 AllGather of the updated parameters stand the gradient's norm (GradNorm), the
 update of the shards (AdamW, moments in fp32 or in 8 bits) and, where the weights
 are gathered in 4 bits, their quantisation and product (dp_mxfp4_*). GradNorm and
-AdamW marshal their pointer arrays once at construction, so a step only enqueues
-launches; the tensors must stay where they are while the object is used.
+AdamW marshal their pointer arrays once at construction; a step checks them and
+enqueues its launches. AdamW's check for overlaps sorts the tensors' addresses (on
+the host: 5 us for 64 tensors, 24 for 300, 0.25 ms for 1,000), so very long lists of
+small tensors are better kept as views of a few buffers. The tensors must stay
+where they are while the object is used.
 """
 from __future__ import annotations
 
@@ -181,7 +184,7 @@ class AdamW:
     def step(self, step: int = 0, ctrl: StepCtrl | None = None, lr: float | None = None,
              stream=None):
         """One update. step: its number (from 1); 0 takes it from ctrl, which
-        also gives the clip factor."""
+        also gives the clip factor. lr: for this step and those after it."""
         self.opts.step = step
         if lr is not None:
             self.opts.lr = lr
