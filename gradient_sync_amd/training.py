@@ -71,7 +71,7 @@ def _at(stream):
     """The handle of `stream`, or of the current stream."""
     if stream is None and _raw_stream is not None:
         return _raw_stream(torch.cuda.current_device())
-    return _stream(stream)
+    return _stream(stream).value or 0
 
 
 def _empty(like, shape, dtype, stream):
@@ -98,7 +98,8 @@ class StepCtrl:
 class GradNorm:
     """Global 2-norm of a list of gradients and the factor that clips it
     (dp_grad_norm). `run` advances ctrl.step, or ctrl.skipped where the norm is
-    not finite, and returns ctrl. It may run on any stream, one run at a time."""
+    not finite, and returns ctrl. It may run on any stream, one run at a time;
+    one that runs on a stream that torch does not own is kept until the run has ended."""
 
     def __init__(self, grads, ctrl: StepCtrl | None = None):
         self._build(grads, ctrl)
@@ -112,13 +113,27 @@ class GradNorm:
         device = self.grads[0].device if self.grads else "cuda"
         self.ctrl = StepCtrl(device=device) if ctrl is None else ctrl
         self.workspace = torch.zeros(GRAD_NORM_WS_BYTES, dtype=torch.uint8, device=device)
+        # streams that the memory of workspace and ctrl is known to be used on
+        self._streams = {torch.cuda.current_stream(self.workspace.device).cuda_stream}
         self._args = (len(self.grads), _counts(self.grads), _pointers(self.grads),
                       _DTYPES[self.grads[0].dtype] if self.grads else 0)
 
     def run(self, max_norm: float = 0.0, stream=None) -> StepCtrl:
+        at = _at(stream)
+        if at not in self._streams:
+            self._streams.add(at)
+            self._use_on(stream)
         _check(lib().dp_grad_norm(*self._args, float(max_norm), self.ctrl.buf.data_ptr(),
-                                  self.workspace.data_ptr(), _at(stream)), "dp_grad_norm")
+                                  self.workspace.data_ptr(), at), "dp_grad_norm")
         return self.ctrl
+
+    def _use_on(self, stream):
+        """The object may be dropped while a run is on its way: its memory is kept for that stream. Not for one
+        that torch does not own (its id is the handle), which may be gone before the object is."""
+        s = torch.cuda.current_stream() if stream is None else stream
+        if isinstance(s, torch.cuda.Stream) and (s.cuda_stream == 0 or s.stream_id != s.cuda_stream):
+            self.workspace.record_stream(s)
+            self.ctrl.buf.record_stream(s)
 
 
 class AdamWOpts(ctypes.Structure):

@@ -159,3 +159,25 @@ def test_a_norm_built_behind_other_work_runs_on_another_stream():
         side.synchronize()
         assert int(ctrl.step) == i + 1 and abs(float(ctrl.norm) - want) <= 1.01 * U * want
         torch.cuda.synchronize()
+
+
+def test_a_norm_dropped_while_its_run_is_on_its_way():
+    """Its workspace and control block go to no one else before the run on the other stream has ended."""
+    g = [torch.full((1000 + i,), 0.5, device=DEV) for i in range(200)]
+    want = math.sqrt(sum(x.numel() for x in g)) * 0.5
+    side = torch.cuda.Stream()
+    busy = torch.ones(1 << 28, device=DEV)
+    torch.cuda.synchronize()
+    for i in range(3):
+        with torch.cuda.stream(side):
+            for _ in range(20):
+                busy.mul_(1.0)
+        norm = dps.GradNorm(g)
+        at, ctrl = norm.workspace.data_ptr(), norm.run(1.0, stream=side)
+        say("dropped norm", i)
+        del norm
+        others = [torch.full((dps.training.GRAD_NORM_WS_BYTES,), 255, dtype=torch.uint8, device=DEV) for _ in range(8)]
+        assert all(o.data_ptr() != at for o in others)
+        side.synchronize()
+        assert abs(float(ctrl.norm) - want) <= 1.01 * U * want and int(ctrl.step) == 1
+        assert all(bool((o == 255).all()) for o in others)
