@@ -4,7 +4,8 @@
 //   e = the smallest with max|x| <= 448 * 2^e, at least -127;  code = e4m3(x 2^-e)
 //
 // rounded to nearest even. The multiplication by 2^-e is exact, so the codes
-// depend on nothing but x. A product sums along the blocks, so a matrix whose
+// depend on nothing but x. The largest finite values round to 256 * 2^120 = 2^128,
+// which expanded is infinite. A product sums along the blocks, so a matrix whose
 // transpose enters another product (the backward pass) is needed in both
 // orientations; one launch reads it once and writes either or both.
 #include "mxfp8_device.h"

@@ -130,7 +130,8 @@ def dp_mxfp8_quantize(x, transposed: str = "no", out: Mxfp8 | None = None,
 
 
 def dp_mxfp8_dequantize(q: Mxfp8, out=None, dtype=torch.bfloat16, stream=None):
-    """The values `q` stands for (exact)."""
+    """The values `q` stands for: exact, but for what lies below bfloat16's smallest subnormal, and 2^128 (held for
+    finite values from 1.9375 * 2^127 on), which becomes an infinity."""
     if not isinstance(q, Mxfp8):
         raise TypeError("dp_mxfp8_dequantize: expected an Mxfp8")
     out = _output(out, (q.rows, q.cols), dtype, q._any(), stream, "out")

@@ -607,7 +607,9 @@ dp_status_t dp_mxfp4_linear(const void *x, int64_t ldx, int x_dt, const void *w,
  *          (so that nothing saturates: one more than floor(log2 max) - 8 where
  *          the largest value's fraction is above 1.75)
  *   code = x 2^-e rounded to nearest even over e4m3
- * A block with a NaN or an infinity is NaN as a whole (scale byte 255).
+ * A block with a NaN or an infinity is NaN as a whole (scale byte 255). The largest
+ * finite values, from 1.9375 * 2^127 on, are held as 2^128: a product takes them as
+ * that number, but fp32 and bf16 have none so large, and expanded they are infinite.
  *
  * Layout of a quantised [rows, cols] matrix (blocks along the columns):
  *   codes  : rows of 128 * ceil(cols / 128) bytes, 16-byte aligned, zero past cols
@@ -623,8 +625,8 @@ dp_status_t dp_mxfp8_quantize(const void *src, int64_t rows, int64_t cols, int64
                               void *stream);
 
 /* The values that a quantised matrix stands for, into dst ([rows, cols], row
- * stride ld). Exact in DP_F32, and in DP_BF16 down to 2^-133, its smallest
- * subnormal, to which smaller parts are rounded. */
+ * stride ld). Exact in DP_F32 (2^128 becomes an infinity), and in DP_BF16 down to
+ * 2^-133, its smallest subnormal, to which smaller parts are rounded. */
 dp_status_t dp_mxfp8_dequantize(const void *codes, const void *scales, int64_t rows, int64_t cols,
                                 void *dst, int64_t ld, int dt, void *stream);
 

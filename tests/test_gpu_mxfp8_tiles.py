@@ -1,5 +1,5 @@
 """Products of 8-bit operands in the large tiles: values of a normal distribution, scales far apart and blocks that are
-NaN, against 64 bits."""
+NaN, against 64 bits; and the largest finite values."""
 import pytest
 import torch
 
@@ -78,3 +78,28 @@ def test_product_of_far_scales_and_nan_blocks(m, n, k, bits):
         assert torch.equal(out.isnan(), nan)
         check_product(out[r][:, keep_c], va[r], vb[keep_c], dtype)
         check_product(out[keep_r][:, c], va[keep_r], vb[c], dtype)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_the_largest_finite_values(dtype):
+    """1.9375 * 2^127, halfway between 240 and 256 times 2^120, and what is above it are held as 2^128 (the even code): beyond
+    fp32, so infinite once expanded, but a number to a product."""
+    least = 1.9375 * 2.0 ** 127
+    below = least - (2.0 ** 104 if dtype == F32 else 2.0 ** 120)
+    x = torch.zeros(4, 64, dtype=dtype)
+    x[:, 3] = torch.tensor([torch.finfo(dtype).max, least, below, -torch.finfo(dtype).max], dtype=torch.float64).to(dtype)
+    held = [2.0 ** 128, 2.0 ** 128, 240 * 2.0 ** 120, -2.0 ** 128]
+    q, qt = dps.dp_mxfp8_quantize(x.to(DEV), transposed="also")
+    for t in (F32, BF16):
+        assert dps.dp_mxfp8_dequantize(q, dtype=t)[:, 3].tolist() == [v if abs(v) < 2.0 ** 128 else v * float("inf") for v in held]
+    for codes in (q.codes[:, 3], qt.codes[3, :4]):
+        assert codes.tolist() == [0x78, 0x78, 0x77, 0xf8]
+    for rows, n in ((4, 5), (70, 50), (2049, 2050), (4001, 4090)):
+        a = torch.zeros(rows, 64, dtype=dtype, device=DEV)
+        a[rows - 4:] = x.to(DEV)
+        say("product of the largest values", rows, n, dtype)
+        for bits in (4, 8):
+            b = quantize(torch.full((n, 64), 2.0 ** -20, device=DEV), bits)
+            out = dps.dp_gemm_mxfp8(dps.dp_mxfp8_quantize(a), b, dtype=F32)
+            assert torch.equal(out[rows - 4:].double(), torch.tensor(held, dtype=torch.float64, device=DEV).mul(2.0 ** -20).unsqueeze(1).expand(4, n))
+            assert not bool(out[:rows - 4].any())
