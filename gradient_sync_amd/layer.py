@@ -10,6 +10,9 @@ One layer, forward and backward:
     dy = dp_gemm_mxfp8(dz8, wt)                            # wt: w's transpose, Mxfp4
     dw = dp_gemm_mxfp8(dz8t, dp_mxfp8_quantize(n.y, transposed="only"))
     dx, dgamma = dp_rms_norm_backward(dy, n.hidden, gamma, n.rstd, dresidual=dr)
+
+The forward product takes the norm's output in 8 bits from fp32, and dw from n.y, which was rounded to its type
+before (bfloat16 here; dtype=torch.float32 leaves that rounding out).
 """
 from __future__ import annotations
 
@@ -143,8 +146,11 @@ def dp_mxfp8_dequantize(q: Mxfp8, out=None, dtype=torch.bfloat16, stream=None):
 
 def dp_gemm_mxfp8(a: Mxfp8, b, out=None, dtype=torch.bfloat16, accumulate: bool = False,
                   stream=None):
-    """a [m, k] in 8 bits times b [n, k] (Mxfp4 or Mxfp8) transposed, fp32 sums;
-    accumulate adds to a float32 `out`."""
+    """a [m, k] in 8 bits times b [n, k] (Mxfp4 or Mxfp8) transposed; accumulate adds to a float32 `out`.
+
+    Sums are kept in fp32, but within each 8 consecutive k the products are first cut to multiples of 2^-13 of the
+    largest one's power of two: on normal values a float32 output is off by 5e-6 of its size with b in 4 bits and by
+    1.5e-5 in 8, where fp32 products and sums leave 3e-8 and 8e-8."""
     if not isinstance(a, Mxfp8) or not isinstance(b, (Mxfp4, Mxfp8)):
         raise TypeError("dp_gemm_mxfp8: a must be an Mxfp8, b an Mxfp4 or an Mxfp8")
     if a.cols != b.cols:

@@ -640,6 +640,8 @@ dp_status_t dp_mxfp8_dequantize(const void *codes, const void *scales, int64_t r
  *   y[m,n]  = Q8(x) . Q4(w)^T               quantised along k
  *   dx[m,k] = Q8(dy) . Q4(w^T)^T            along n
  *   dw[n,k] = Q8(dy^T) . Q8(x^T)^T          along m (the tokens)
+ * A norm (dp_rms_norm) gives Q8(x) from its fp32 values; Q8(x^T) is quantised from
+ * its plain output, rounded to y_dt before.
  */
 dp_status_t dp_gemm_mxfp8(const void *a, const void *a_scales, const void *b, const void *b_scales,
                           int b_bits, void *c, int64_t m, int64_t n, int64_t kk, int c_dt,
