@@ -552,7 +552,8 @@ __global__ __launch_bounds__(kBlock<TPR>) void rms_norm_grad_kernel(const RmsNor
 {
     grad_rows<DT, YT, TPR, NCH, ONCE ? kOnce : kOrdinary>(p);
 }
-// rows of fewer than 8 elements
+// Rows of fewer than 8 elements, which have no last 8 to load. One lane of a wave works, and loads element by element:
+// 100000 x 7 bf16 245 us, 100000 x 100 68.
 template <int DT, int YT>
 __global__ __launch_bounds__(kNT) void rms_norm_grad_short_kernel(const RmsNormGradParams p)
 {
@@ -661,12 +662,12 @@ hipError_t launch_grad(const RmsNormGradParams &p, hipStream_t stream)
     const int parts = grad_parts(p.rows, p.cols);
     if (p.rows == 0) {
         // dw is the sum of nothing
+    } else if (p.cols < 8) {                         // parts are those of a wave a row
+        rms_norm_grad_short_kernel<DT, YT><<<parts, kNT, 0, stream>>>(p);
     } else if (held(p.cols)) {
         by_length(p.rows, p.cols, [&](auto tpr, auto nch) {
             constexpr int TPR = decltype(tpr)::value, NCH = decltype(nch)::value;
-            if (p.cols < 8)                          // then parts are those of a wave a row
-                rms_norm_grad_short_kernel<DT, YT><<<parts, kNT, 0, stream>>>(p);
-            else if (once && TPR > 64)
+            if (once && TPR > 64)
                 rms_norm_grad_kernel<DT, YT, TPR, NCH, (TPR > 64)><<<parts, kBlock<TPR>, 0, stream>>>(p);
             else
                 rms_norm_grad_kernel<DT, YT, TPR, NCH, false><<<parts, kBlock<TPR>, 0, stream>>>(p);
