@@ -73,8 +73,8 @@ __device__ __forceinline__ void mx_pin(unsigned &x)
 {
     asm volatile("" : "+v"(x));
 }
-// 32 cycles: longer than the instruction takes to write its sums (16) and than
-// a vector instruction's result takes to reach it
+// 32 wait states: longer than the instruction takes until its sums may be read (the compiler leaves 8 behind one with
+// operands in 4 bits, 12 with one in 8) and than a vector instruction's result takes to reach it
 __device__ __forceinline__ void mx_settle() { asm volatile("s_nop 15\n\ts_nop 15" ::: "memory"); }
 
 
