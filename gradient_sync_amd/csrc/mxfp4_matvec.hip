@@ -6,8 +6,9 @@
 // they are is free as long as both hold the same. A lane takes a whole block, 32 codes
 // of a row of B, and expands them eight at a time: e2m1 times the block's power of two is
 // exact in bf16. x in bf16 enters as it is. x in fp32 is the sum of three
-// bf16 values, exactly (its 24 bits cut into 8, 8 and 8), and takes three
-// instructions.
+// bf16 values (its 24 bits cut into 8, 8 and 8), and takes three
+// instructions; exactly so from 2^-110 on, below which the last of its bits are under
+// bf16's smallest, 2^-133, and lost.
 #include <algorithm>
 #include <type_traits>
 
@@ -31,8 +32,8 @@ __device__ __forceinline__ bf16x8 expand8(unsigned w, float scale)
 }
 
 // 8 values of x of a row, from `at` on, the first n of them (zero past them), as bf16 addends: one, or three of fp32, cut into
-// the upper 16 bits, the upper 16 of what these leave, and the rest, exactly. An infinity leaves NaN; SAFE: nothing
-// of an infinity or a NaN is left, and a NaN keeps a bit among its upper 16.
+// the upper 16 bits, the upper 16 of what these leave, and the upper 16 of the rest (all of it, from 2^-110 on). An
+// infinity leaves NaN; SAFE: nothing of an infinity or a NaN is left, and a NaN keeps a bit among its upper 16.
 template <int XT> constexpr int kPlanes = XT == kF32 ? 3 : 1;
 template <int XT> struct Values { u32x4 v[XT == kF32 ? 2 : 1]; };
 

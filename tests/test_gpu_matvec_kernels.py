@@ -66,3 +66,22 @@ def test_all_24_bits_of_x_enter_every_kernel(m, n, k):
         x[r, at] = v
         want = v.unsqueeze(1) * w[:, at].t()
         assert torch.equal(dps.dp_mxfp4_matvec(x, q, dtype=F32), want)
+
+
+@pytest.mark.parametrize("m,n,k", [(1, 300, 1030), (2, 300, 4700), (9, 1000, 1030), (64, 8200, 1030)])
+def test_small_values_of_x(m, n, k):
+    """fp32 values from 2^-110 on enter with all their bits (the last of which is 2^-133, bf16's smallest number), smaller ones
+    with those from 2^-133 on; zero and what is below that are nothing."""
+    g = torch.Generator(device=DEV).manual_seed(m)
+    w = torch.full((n, k), 2.0 ** 40, device=DEV)
+    q = dps.dp_mxfp4_quantize(w)
+    r = torch.arange(m, device=DEV)
+    for e in (-108, -109, -110, -111, -118, -126, -127):         # -127: fp32's own subnormal numbers
+        bits = torch.randint(0, 1 << 23, (m,), generator=g, device=DEV) | 1 | (e + 127) << 23
+        v = bits.int().view(F32)
+        x = torch.zeros(m, k, device=DEV)
+        x[r, (r * 97 + 5) % k] = v
+        say("matvec, small values", m, n, k, e)
+        y = dps.dp_mxfp4_matvec(x, q, dtype=F32).double() * 2.0 ** -40
+        kept = (v.double() * 2.0 ** 133).trunc() * 2.0 ** -133
+        assert torch.equal(y, (v.double() if e >= -110 else kept).unsqueeze(1).expand(m, n))
