@@ -478,8 +478,8 @@ hipError_t launch_tile(const MxGemmParams &p, hipStream_t stream)
     return hipGetLastError();
 }
 
-// Microseconds, fitted to 250 shapes (m 1 .. 4096, n 64 .. 14336, k 128 .. 14336), most within a tenth
-// of what was measured; the second figure of a pair is for B in 8 bits:
+// Microseconds, fitted to 250 shapes (m 1 .. 4096, n 64 .. 14336, k 128 .. 14336); a half to two thirds of the estimates
+// are within a tenth of what was measured. The second figure of a pair is for B in 8 bits:
 // few rows: what a workgroup reads of B and of A's rows, one alone and 256 of them together;
 // tiles of 64, 128: a stage takes a lone workgroup so long, and 256 of them together so long besides their
 //   begin and end; with tiles of 64, which few rows take too, B comes at 4.5 TB/s;
@@ -487,6 +487,10 @@ hipError_t launch_tile(const MxGemmParams &p, hipStream_t stream)
 // Where they differ most (us by few rows, 64, 128, 256): 1 x 4096 x 14336 10.9, 25.8; 32 x 14336 x 4096 21.4,
 // 11.3; 64 x 14336 x 4096 35.4, 9.5, 15.5; 201 x 4096 x 4096 30.1, 8.9, 14.2, 36.4; 1024 x 4096 x 4096 130, 25.5, 18.9, 38.0;
 // 4096 x 4096 x 4096 -, -, 63.4, 47.0.
+// Of 402 choices (17 .. 1024 rows, weights in cache) 30 cost more than a tenth over the best of few rows, 64 and 128, and 17
+// more than a fifth. Tiles of 128 are taken too early then, with B in 8 bits over wide weights, as its bytes count against
+// tiles of 64 alone (us by 128, taken, and by 64: 64 x 14336 x 14336 49.5, 33.2; 64 x 14336 x 4096 17.7, 12.9; 64 x 14336 x
+// 2000 10.3, 7.1), with B in 4 bits less often (201 x 4096 x 512 5.6, 4.2; 128 x 14336 x 4096 17.2, 14.0).
 template <int CT, int BB>
 hipError_t launch_typed(const MxGemmParams &p, hipStream_t stream)
 {
