@@ -219,10 +219,10 @@ template <int WB, int BB> struct Plan {
 //      buffer, t + 1 is read
 // is its only barrier (201 x 4096 x 4096: 8.9 us, with two buffers 14.2 in tiles of 128).
 //
-// Measured: 4096 x 4096 x 4096 with a 4-bit B 51 us (2.7 PFLOP/s; B in 8 bits 52, C in fp32 62), 8192 x 14336 x 4096
-// 321 to 369 by the card's clock (2.6 to 3.0). A loop of these instructions alone reaches 3.7 on uniformly
+// Measured: 4096 x 4096 x 4096 with a 4-bit B 50 to 51 us (2.7 PFLOP/s; B in 8 bits 51 to 52, C in fp32 56 to 62), 8192 x
+// 14336 x 4096 321 to 374 by the card's clock (2.6 to 3.0). A loop of these instructions alone reaches 3.7 on uniformly
 // random codes and 4.0 on those of a normal distribution, in 4 bits or 8: the 8-bit operand's rate and the card's power
-// bound the large product; its matrix units are busy 66 to 74% of the cycles and its waves wait in 12%.
+// bound the large product; its matrix units are busy 66 to 74% of the cycles and its waves wait in 13%.
 //
 // Scales come as one 32-bit load per 16 rows and four stages (512 of K), loaded in
 // the third stage of the four before. K is walked in fours of stages; a stage past the

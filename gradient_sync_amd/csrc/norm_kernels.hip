@@ -395,8 +395,8 @@ __global__ __launch_bounds__(kNT) void rms_norm_long_kernel(const RmsNormParams 
 
 // f(threads a row, chunks a thread) for rows of `cols` elements: one chunk, or two, four of 8 elements in as
 // many threads as that takes, so that a CU has many rows on their way; with many rows a wave to a row of up to
-// two. Measured, us for 8192 x 4096 bf16 with the residual and 8-bit output: a wave a row (8 chunks) 64.5, 256 threads (2) 46.1,
-// 512 (1) 46.0; its gradients 175, 50.9, 47.0. 4096 x 8192: 256 threads (4) 48.7, 512 (2) 45.3; gradients 52.9, 48.6.
+// two. Measured, us for 8192 x 4096 bf16 with the residual and 8-bit output: a wave a row (8 chunks) 66.2, 256 threads (2) 43.9,
+// 512 (1) 45.6; its gradients 63.2, 48.9, 47.7. 4096 x 8192: 256 threads (4) 49.4, 512 (2) 44.6; gradients 49.7, 48.7.
 template <typename F>
 void by_length(long long rows, long long cols, F f)
 {
@@ -436,14 +436,14 @@ hipError_t launch_norm(const RmsNormParams &p, hipStream_t stream)
 
 // ------------------------------------------------------------ gradients
 
-// Most workgroups whose sums of dw a second launch adds up. 8192 x 4096 bf16: 128 67.3 us, 192 52.1, 256 46.6, 512
-// 49.6; 1000 x 2049 fp32: 20.4, 17.9, 14.8, 16.0.
+// Most workgroups whose sums of dw a second launch adds up. 8192 x 4096 bf16: 128 67.7 us, 192 53.1, 256 47.7, 512
+// 50.6; 1000 x 2049 fp32: 13.8, 13.4, 12.4, 14.9.
 constexpr int kGradGroups = 256;
 
 // The rows of a workgroup follow one another by the grid's size, so that each has its sums
 // of dw in registers; the sums of a workgroup's waves meet in LDS. The next row is loaded before this one's sum.
-// Bound by HBM: 8192 x 4096 bf16 with the residual 41 us, its 272 MB, three quarters of them read, at 6.6 TB/s; with
-// the launch that sums dw 46.7.
+// Bound by HBM: 8192 x 4096 bf16 with the residual 42 to 46 us by the card, its 273 MB, three quarters of them read, at 5.9
+// to 6.5 TB/s; with the launch that sums dw 46.7 to 47.7.
 template <int DT, int YT, int TPR, int NCH, int HOW>
 __device__ __forceinline__ void grad_rows(const RmsNormGradParams &p)
 {
@@ -553,7 +553,7 @@ __global__ __launch_bounds__(kBlock<TPR>) void rms_norm_grad_kernel(const RmsNor
     grad_rows<DT, YT, TPR, NCH, ONCE ? kOnce : kOrdinary>(p);
 }
 // Rows of fewer than 8 elements, which have no last 8 to load. One lane of a wave works, and loads element by element:
-// 100000 x 7 bf16 245 us, 100000 x 100 68.
+// 100000 x 7 bf16 245 to 249 us, 100000 x 100 68.
 template <int DT, int YT>
 __global__ __launch_bounds__(kNT) void rms_norm_grad_short_kernel(const RmsNormGradParams p)
 {
@@ -652,9 +652,9 @@ int grad_parts(long long rows, long long cols)
 }
 
 // From 128 MiB on, rows of more than a wave are read nontemporal, so that they do not push one another out of the 256
-// MiB cache behind the L2s. 8192 x 4096 bf16 with the residual, 192 MiB, over and over: 46.7 us against 52.0; 2048 x
-// 4096, 48 MiB, in turn with others: 18.2 against 16.2. Rows of a wave, 65536 x 512: bf16 61.4 against 61.1, fp32 104 against
-// 96.
+// MiB cache behind the L2s; with rows loaded whole that gives 1% (nontemporal against ordinary, with the residual, in turn
+// with others: 8192 x 4096 bf16, 192 MiB, 47.5 us against 48.1, fp32 96.9 against 98.6; 2048 x 4096 bf16, 48 MiB, 17.8 against
+// 16.3). Rows of a wave, 65536 x 512: bf16 59.7 against 60.3, fp32 105 against 95.
 template <int DT, int YT>
 hipError_t launch_grad(const RmsNormGradParams &p, hipStream_t stream)
 {
